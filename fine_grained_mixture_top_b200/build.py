@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 
-SOURCES = ["moe_api.cu", "moe_gemm.cu", "moe_route.cu", "moe_agg.cu", "moe_mx.cu", "moe_ep.cu", "moe_debug.cu"]
+SOURCES = ["moe_api.cu", "moe_gemm.cu", "moe_route.cu", "moe_agg.cu", "moe_mx.cu", "moe_ep.cu", "moe_debug.cu",
+           "moe_move.cu"]
 # the debug build: the same sources with the device-side routing checks on
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libmoe_debug.so")

@@ -524,9 +524,9 @@ inline int grid_for(int64_t max_tiles, int sms) { return (int)std::max<int64_t>(
 // it (read back through moe_last_error).
 thread_local char g_last_error[512] = "";
 
-moe_status cuda_failed(cudaError_t e, int line) {
-  std::snprintf(g_last_error, sizeof(g_last_error), "%s (%s) at moe_api.cu:%d%s%s", cudaGetErrorName(e),
-                cudaGetErrorString(e), line, g_launch_diag[0] ? "; " : "", g_launch_diag);
+moe_status cuda_failed(cudaError_t e, int line, const char* file = "moe_api.cu") {
+  std::snprintf(g_last_error, sizeof(g_last_error), "%s (%s) at %s:%d%s%s", cudaGetErrorName(e),
+                cudaGetErrorString(e), file, line, g_launch_diag[0] ? "; " : "", g_launch_diag);
   g_launch_diag[0] = 0;
   return MOE_ERR_CUDA;
 }
@@ -563,6 +563,24 @@ ProfScope::ProfScope(cudaStream_t s, const char* name) : stream(s) {
 ProfScope::~ProfScope() {
   if (slot >= 0) cudaEventRecord(g_prof[slot].b, stream);
   nvtxRangePop();
+}
+
+bool api_device(ApiDevice* out) {
+  if (!device_state(&out->dev, &out->status, &out->sms)) return false;
+  out->spin_limit = g_spin_limit;
+  return true;
+}
+moe_status api_cuda_failed(cudaError_t e, const char* file, int line) { return cuda_failed(e, line, file); }
+bool api_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t planes, uint64_t rows,
+                    uint64_t cols, uint64_t row_stride, uint64_t plane_stride, uint32_t box_rows, uint32_t box_cols) {
+  if (!get_encode()) return false;
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {row_stride, plane_stride};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(m, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 }  // namespace moe
 

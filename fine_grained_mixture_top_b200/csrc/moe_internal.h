@@ -1,11 +1,13 @@
 // Internal launch interface between the C-ABI layer (moe_api.cu) and the
 // kernel translation units.  Not part of the public ABI.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 #include <utility>
 
 #include "gemm.cuh"
+#include "moe.h"
 
 namespace moe {
 
@@ -88,6 +90,20 @@ struct ApiRange {
   explicit ApiRange(const char* name);
   ~ApiRange();
 };
+
+// ---- shared by the files that hold C-ABI entry points (moe_api.cu)
+struct ApiDevice {
+  int dev, sms;          // the current device, CTAs of a persistent GEMM
+  int* status;           // its status word
+  long long spin_limit;  // clock cycles of a bounded wait
+};
+bool api_device(ApiDevice* out);
+// Records a failed CUDA call for moe_last_error and returns MOE_ERR_CUDA.
+moe_status api_cuda_failed(cudaError_t e, const char* file, int line);
+// Tensor map of a [planes, rows, cols] array with strides in bytes, boxes of
+// one plane, and zeros outside; false if it cannot be encoded.
+bool api_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t planes, uint64_t rows,
+                    uint64_t cols, uint64_t row_stride, uint64_t plane_stride, uint32_t box_rows, uint32_t box_cols);
 
 // ---- routing (moe_route.cu)
 struct RouteArgs {

@@ -95,6 +95,14 @@ def lib() -> ctypes.CDLL:
         L.moe_ep_combine.argtypes = [P(MoeDims), P(MoeOpts), P(MoeRouting), c_void_p, c_void_p, c_void_p, c_void_p]
         L.moe_router_backward.argtypes = [P(MoeDims), P(MoeOpts), c_void_p, c_void_p, P(MoeRouting), c_void_p,
                                           c_void_p, c_void_p, c_void_p, c_void_p, ctypes.c_size_t, c_void_p]
+        L.moe_sort_sizes.argtypes = [c_int64, c_int32, c_int32, P(c_int64), P(c_int64), P(ctypes.c_size_t)]
+        L.moe_sort_pairs.argtypes = [c_int64, c_int32, c_int32, P(MoeRouting), c_void_p, ctypes.c_size_t, c_void_p]
+        L.moe_permute.argtypes = [c_int64, c_int32, P(MoeRouting), c_int32, c_int64, c_void_p, c_int64, c_void_p,
+                                  c_int64, c_void_p]
+        L.moe_permute_bwd.argtypes = L.moe_permute.argtypes
+        L.moe_unpermute.argtypes = L.moe_permute.argtypes
+        L.moe_unpermute_bwd.argtypes = [c_int64, c_int32, c_int32, P(MoeRouting), c_int32, c_int64, c_void_p, c_int64,
+                                        c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p]
         L.moe_mx_quantize_rows.argtypes = [c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p]
         L.moe_mx_quantize_cols.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p]
         L.moe_get_status.argtypes = [c_void_p, P(c_int32)]
@@ -118,7 +126,8 @@ def lib() -> ctypes.CDLL:
                   "moe_get_status", "moe_set_spin_limit", "moe_selftest_wait_timeout", "moe_backward_ev",
                   "moe_set_sm_budget", "moe_mx_quantize_rows", "moe_mx_quantize_cols", "moe_forward_mxfp8",
                   "moe_route_given", "moe_ep_pack", "moe_ep_combine", "moe_router_backward",
-                  "moe_mx_quantize_weights", "moe_forward_mxfp8_q"):
+                  "moe_mx_quantize_weights", "moe_forward_mxfp8_q", "moe_sort_sizes", "moe_sort_pairs", "moe_permute",
+                  "moe_permute_bwd", "moe_unpermute", "moe_unpermute_bwd"):
             getattr(L, f).restype = c_int32
         _lib = L
     return _lib
@@ -300,6 +309,188 @@ def mx_quantize_cols(w, stream=None):
     _check(lib().moe_mx_quantize_cols(_ptr(w), E, K, N, _ptr(codes), _ptr(scales), _stream(stream)),
            "moe_mx_quantize_cols")
     return codes, scales
+
+
+# ----------------------------------------------------------------------------
+# Rows sorted by expert and back.  These check their tensors, allocate what the
+# caller leaves out, and run on the tensors' device.
+
+_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2, "torch.float8_e4m3fn": 3}
+
+
+def _dtype_code(t, what: str, most: int = 2) -> int:
+    code = _DTYPES.get(str(t.dtype), 99)
+    if code > most:
+        raise TypeError(f"{what}: {t.dtype} is not supported")
+    return code
+
+
+def _want(cond: bool, message: str):
+    if not cond:
+        raise ValueError(message)
+
+
+def _width(t, name: str) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
+    return t.shape[1]
+
+
+def _matrix(t, name: str, rows: int, cols: int, device, dtype=None) -> int:
+    """Check a [rows, cols] tensor with unit column stride; returns its row
+    stride.  (Messages are made only for a refusal: these checks run before
+    calls of a few microseconds.)"""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    if rows == 0 or cols == 0:
+        return cols
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if rows == 1:
+        return cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap (stride {ld} for {cols} columns)")
+    return ld
+
+
+def _away(device) -> bool:
+    """Is `device` another than the current one?  (It then has to be made current for the call.)"""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}: a CUDA device is needed")
+    return torch.cuda.current_device() != device.index
+
+
+def _on(device, fn, *args, **kw):
+    import torch
+    with torch.cuda.device(device):
+        return fn(*args, **kw)
+
+
+def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=None, stream=None) -> Routing:
+    """Sort the choices topk_idx [T, K] (int32; outside [0, E): dropped) with
+    gates topk_gate [T, K] (fp32) by expert: see moe_sort_pairs in moe.h.  A
+    Routing of an earlier call with the same T, K and E can be given again as
+    `routing`; it is overwritten.  ws: a uint8 workspace of moe_sort_sizes'
+    bytes (default: allocated)."""
+    import torch
+    dev = topk_idx.device
+    K = _width(topk_idx, "topk_idx")
+    T = topk_idx.shape[0]
+    for t, name, dt in ((topk_idx, "topk_idx", torch.int32), (topk_gate, "topk_gate", torch.float32)):
+        if _matrix(t, name, T, K, dev, dt) != K:
+            raise ValueError(f"{name}: must be contiguous")
+    if _away(dev):
+        return _on(dev, sort_pairs, topk_idx, topk_gate, E, routing, ws, stream)
+    if routing is None or ws is None:
+        P, R, need = c_int64(0), c_int64(0), ctypes.c_size_t(0)
+        _check(lib().moe_sort_sizes(T, E, K, ctypes.byref(P), ctypes.byref(R), ctypes.byref(need)), "moe_sort_sizes")
+        if ws is None and need.value:
+            ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        if routing is None:
+            i32, f32 = torch.int32, torch.float32
+            sizes = {"tok_ptr": (T + 1, i32), "pair_expert": (P.value, i32), "pair_gate": (P.value, f32),
+                     "pair_row": (P.value, i32), "counts": (E, i32), "offsets": (E + 1, i32),
+                     "row_tok": (R.value, i32), "row_gate": (R.value, f32), "tile_expert": (R.value // 128, i32)}
+            # at least one element each, so that every pointer is one even without tokens
+            whole = {k: torch.empty(max(n, 1), dtype=dt, device=dev) for k, (n, dt) in sizes.items()}
+            st = MoeRouting(**{k: _ptr(t) for k, t in whole.items()}, P_max=P.value, R_max=R.value)
+            routing = Routing({**{k: t[:sizes[k][0]] for k, t in whole.items()}, "logits": None, "probs": None,
+                               "pair_dS": None}, st)
+    elif ws.dtype != torch.uint8 or ws.device != dev:
+        raise ValueError(f"ws: uint8 on {dev} expected")
+    r, st = routing.tensors, routing.struct
+    if r["tok_ptr"].shape[0] != T + 1 or r["counts"].shape[0] != E or r["tok_ptr"].device != dev:
+        raise ValueError("routing: made for another T, E or device")
+    r["topk_idx"], r["topk_gate"] = topk_idx, topk_gate
+    st.topk_idx, st.topk_gate = _ptr(topk_idx), _ptr(topk_gate)
+    _check(lib().moe_sort_pairs(T, E, K, ctypes.byref(st), _ptr(ws), 0 if ws is None else ws.numel(),
+                                _stream(stream)), "moe_sort_pairs")
+    return routing
+
+
+def _routed(routing: Routing):
+    """(T, E, R_max, device) of a routing."""
+    r = routing.tensors
+    tok_ptr = r["tok_ptr"]
+    return tok_ptr.shape[0] - 1, r["counts"].shape[0], routing.struct.R_max, tok_ptr.device
+
+
+def permute(routing: Routing, src, rows=None, stream=None):
+    """rows [R_max, width]: src [T, width] in expert order, zeros in the padding
+    rows.  Rows past the last expert's segment are left as they were (in a
+    tensor allocated here: undefined)."""
+    T, E, R, dev = _routed(routing)
+    code = _dtype_code(src, "src", 3)
+    width = _width(src, "src")
+    ld = _matrix(src, "src", T, width, dev)
+    if _away(dev):
+        return _on(dev, permute, routing, src, rows, stream)
+    if rows is None:
+        rows = src.new_empty((R, width))
+    ldr = _matrix(rows, "rows", R, width, dev, src.dtype)
+    _check(lib().moe_permute(T, E, ctypes.byref(routing.struct), code, width, _ptr(src), ld, _ptr(rows), ldr,
+                             _stream(stream)), "moe_permute")
+    return rows
+
+
+def _sum_rows(fn, what, routing, rows, out, stream):
+    T, E, R, dev = _routed(routing)
+    code = _dtype_code(rows, "rows")
+    width = _width(rows, "rows")
+    ld = _matrix(rows, "rows", R, width, dev)
+    if _away(dev):
+        return _on(dev, _sum_rows, fn, what, routing, rows, out, stream)
+    if out is None:
+        out = rows.new_empty((T, width))
+    ldo = _matrix(out, "out", T, width, dev, rows.dtype)
+    _check(fn(T, E, ctypes.byref(routing.struct), code, width, _ptr(rows), ld, _ptr(out), ldo, _stream(stream)), what)
+    return out
+
+
+def permute_bwd(routing: Routing, drows, dsrc=None, stream=None):
+    """Gradient of permute: dsrc [T, width], each token's rows of drows summed."""
+    return _sum_rows(lib().moe_permute_bwd, "moe_permute_bwd", routing, drows, dsrc, stream)
+
+
+def unpermute(routing: Routing, rows, out=None, stream=None):
+    """out [T, width]: each token's rows weighted by their gates and summed."""
+    return _sum_rows(lib().moe_unpermute, "moe_unpermute", routing, rows, out, stream)
+
+
+def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: bool = False, stream=None):
+    """Gradients of unpermute: (drows [R_max, width], dgate).  dgate is [T, K]
+    in the places of topk_idx, 0 for dropped choices; with pairs=True it is
+    [P_max] in pair order (for moe_token_round's routings), where entries past
+    the pairs in use are left as they were."""
+    import torch
+    T, E, R, dev = _routed(routing)
+    code = _dtype_code(rows, "rows")
+    width = _width(rows, "rows")
+    ld = _matrix(rows, "rows", R, width, dev)
+    ldo = _matrix(dout, "dout", T, width, dev, rows.dtype)
+    K = routing.tensors["topk_idx"].shape[1]
+    if _away(dev):
+        return _on(dev, unpermute_bwd, routing, dout, rows, drows, dgate, pairs, stream)
+    if drows is None:
+        drows = rows.new_empty((R, width))
+    ldd = _matrix(drows, "drows", R, width, dev, rows.dtype)
+    shape = (routing.struct.P_max,) if pairs else (T, K)
+    if dgate is None:
+        dgate = torch.empty(shape, dtype=torch.float32, device=dev)
+    elif dgate.dtype != torch.float32:
+        raise TypeError(f"dgate: {dgate.dtype}, expected torch.float32")
+    elif dgate.shape != shape or dgate.device != dev or not dgate.is_contiguous():
+        raise ValueError(f"dgate: contiguous {shape} on {dev} expected")
+    _check(lib().moe_unpermute_bwd(T, E, K, ctypes.byref(routing.struct), code, width, _ptr(dout), ldo, _ptr(rows),
+                                   ld, _ptr(drows), ldd, _ptr(dgate) if pairs else None,
+                                   None if pairs else _ptr(dgate), _stream(stream)), "moe_unpermute_bwd")
+    return drows, dgate
 
 
 def moe_set_sm_budget(sms: int):

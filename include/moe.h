@@ -312,6 +312,72 @@ moe_status moe_mx_quantize_rows(const void* in, int64_t rows, int32_t K, void* c
 moe_status moe_mx_quantize_cols(const void* in, int32_t E, int32_t K, int32_t N, void* codes, void* scales,
                                 void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rows sorted by expert and back, as calls of their own: for experts that are
+ * not this library's (another activation, an adapter, an 8-bit product), for
+ * capacity limits that drop choices, and for any element type.  Each works on
+ * every moe_routing this library builds (moe_sort_pairs, moe_route,
+ * moe_route_given, moe_token_round).
+ *
+ * Row tensors here are [.., width] with rows `ld` elements apart (ld >= width)
+ * and need only be aligned to their elements (multiples of 16 bytes are
+ * faster).  In and out tensors must not overlap.
+ * E <= 1024; T * K, the pairs and the rows below 2^31; width <= 2^20.
+ */
+typedef enum {
+  MOE_BF16 = 0,
+  MOE_F16 = 1,
+  MOE_F32 = 2,
+  MOE_E4M3 = 3 /* 8-bit codes: moe_permute only */
+} moe_dtype;
+
+/*
+ * Sort of a caller's selection.  rt->topk_idx[T,K] (i32) and topk_gate[T,K]
+ * (f32) are inputs (4-byte aligned); a choice outside [0, E) -- the usual -1 --
+ * is dropped: it gets no pair and no row, and a token may lose all its
+ * choices.  A token may choose an expert twice and then has two rows there.
+ * Fills tok_ptr, pair_expert, pair_gate, pair_row (the kept choices in (t, k)
+ * order), counts, offsets, row_tok, row_gate, tile_expert as moe_routing
+ * describes them (rows of an expert in (t, k) order), and beyond the used rows
+ * and pairs, up to R_max and P_max: row_tok, tile_expert, pair_row and
+ * pair_expert -1, row_gate and pair_gate 0.  logits and probs are not touched.
+ * moe_sort_sizes: capacities (P_max = T K, R_max a multiple of 128) and the
+ * bytes of ws, which may be 0 (then ws may be NULL).  1 <= K <= 32; T may be 0.
+ */
+moe_status moe_sort_sizes(int64_t T, int32_t E, int32_t K, int64_t* P_max, int64_t* R_max, size_t* ws_bytes);
+moe_status moe_sort_pairs(int64_t T, int32_t E, int32_t K, const moe_routing* rt, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * rows[r] = src[row_tok[r]] for the rows in use, padding rows inside them 0;
+ * rows from offsets[E] on are left as they were.  Any dtype (bits are moved).
+ * src [T, width], rows [rt->R_max, width].
+ * moe_permute_bwd: dsrc[t] = sum over token t's pairs of drows[pair_row],
+ * fp32 sums in pair order, rounded once; 0 for a token without pairs.
+ */
+moe_status moe_permute(int64_t T, int32_t E, const moe_routing* rt, moe_dtype type, int64_t width, const void* src,
+                       int64_t ld_src, void* rows, int64_t ld_rows, void* stream);
+moe_status moe_permute_bwd(int64_t T, int32_t E, const moe_routing* rt, moe_dtype type, int64_t width,
+                           const void* drows, int64_t ld_drows, void* dsrc, int64_t ld_dsrc, void* stream);
+
+/*
+ * out[t] = sum over token t's pairs of pair_gate * rows[pair_row] (fp32 sums in
+ * pair order, rounded once; 0 for a token without pairs).
+ * moe_unpermute_bwd, given dout[T, width] and the forward's rows:
+ *   drows[r] = row's gate * dout[its token], padding rows in use 0, rows from
+ *   offsets[E] on left as they were;
+ *   the gate gradients <dout[t], rows[r]> (fp32) as pair_dgate[P_max] in pair
+ *   order (entries past the pairs in use are left) and/or topk_dgate[T,K] in
+ *   the places of rt->topk_idx, 0 for dropped choices (each nullable;
+ *   topk_dgate is for routings whose pairs are the kept choices in slot order:
+ *   any but moe_token_round's).
+ */
+moe_status moe_unpermute(int64_t T, int32_t E, const moe_routing* rt, moe_dtype type, int64_t width, const void* rows,
+                         int64_t ld_rows, void* out, int64_t ld_out, void* stream);
+moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing* rt, moe_dtype type, int64_t width,
+                             const void* dout, int64_t ld_dout, const void* rows, int64_t ld_rows, void* drows,
+                             int64_t ld_drows, float* pair_dgate, float* topk_dgate, void* stream);
+
 /*
  * Synchronises `stream`, returns the device status word (MOE_OK if no kernel
  * reported an error since the last call) and clears it.  *where (nullable)
