@@ -1,0 +1,470 @@
+// E4M3 quantization with one fp32 scale per block of 128 values: rows (1 x 128
+// blocks, gathered by a routing or behind the SwiGLU product if asked),
+// columns (128 x 1 blocks, written transposed) and 128 x 128 blocks of expert
+// weights (as they are, or transposed).
+//
+// For a block's largest magnitude m (at least 2^-110, so that neither scale
+// nor factor leaves the normal range): scale = m / 448, code = e4m3(x * (448 / m)),
+// both divisions in fp32, one per block.  448 is E4M3's largest value, so no
+// code saturates.  Every kernel reads its input once and writes a byte per
+// value: bound by those bytes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "fp8_gemm.cuh"
+#include "moe.h"
+#include "moe_internal.h"
+#include "rows.cuh"
+
+namespace moe {
+namespace {
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+constexpr int kBlk = 128;  // values per scale
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 7.7037197775489434e-34f;  // 2^-110
+
+__device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) { return cvt2(a, b) | cvt2(c, d) << 16; }
+
+// Eight values of a row from element e0 on (a multiple of 8), zeros outside
+// [0, width).  FAST: the row's 16-byte pieces are aligned and width is a
+// multiple of 8.  Otherwise pieces whose windows stay inside the row come from
+// two windows each, and those at its ends element by element.
+template <typename T, bool FAST>
+__device__ __forceinline__ void load8(const T* row, int e0, int width, float (&x)[8]) {
+  constexpr int V = kVec<T>;
+  if (FAST ? e0 < width : (e0 >= V - 1 && e0 + 8 + V - 1 <= width)) {
+    Piece<T> p[8 / V];
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i) p[i] = load_piece<T, FAST>(row + e0 + i * V);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_float(p[i / V].x[i % V]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = !FAST && e0 + i < width ? to_float(row[e0 + i]) : 0.f;
+}
+template <typename T>
+bool fast_rows(const void* in, int64_t ld, int64_t width) {
+  return aligned16(in) && ld * (int64_t)sizeof(T) % 16 == 0 && width % 8 == 0;
+}
+
+struct QuantArgs {
+  int64_t rows, ld_in, ld_codes, ld_scales;
+  int cols, kblocks;           // blocks of a row (rows kernel)
+  const int* row_src;          // nullable: the input row of each row, -1: zeros
+  const int* rows_used;        // nullable: rows from here on are left as they are
+  uint8_t* codes;
+  float* scales;
+  int64_t plane_in, plane_codes, plane_scales;  // expert weights: elements per expert
+};
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+
+// Rows: a block of 128 values per half warp, 8 per lane; each thread has two
+// blocks, 16 apart in a thread block's run of 32, in flight at once.
+template <typename T, bool FAST, bool SWIGLU>
+__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const QuantArgs a, const T* __restrict__ in) {
+  pdl_wait();
+  const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const int64_t used = a.rows_used ? min((int64_t)__ldg(a.rows_used), a.rows) : a.rows;
+  float x[2][8];
+  int64_t row[2];
+  int kb[2];
+  bool live[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t unit = blockIdx.x * 32u + i * 16u + half;
+    const uint32_t r = unit / (uint32_t)a.kblocks;
+    row[i] = r;
+    kb[i] = (int)(unit - r * (uint32_t)a.kblocks);
+    live[i] = row[i] < used;
+    int64_t from = row[i];
+    if (live[i] && a.row_src) from = __ldg(a.row_src + row[i]);
+    const int e0 = kb[i] * kBlk + 8 * l;
+    if (live[i] && from >= 0) {
+      const T* src = in + from * a.ld_in;
+      load8<T, FAST>(src, e0, a.cols, x[i]);
+      if constexpr (SWIGLU) {  // up projection behind the gate's `cols` columns
+        float u[8];
+        load8<T, FAST>(src + a.cols, e0, a.cols, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i][j] = silu_mul(x[i][j], u[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float m = kAmaxFloor;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[i][j]));
+#pragma unroll
+    for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    if (!live[i]) continue;
+    const float f = kE4m3Max / m;
+    const int e0 = kb[i] * kBlk + 8 * l;
+    uint8_t* out = a.codes + row[i] * a.ld_codes + e0;
+    const uint2 q = make_uint2(cvt4(x[i][0] * f, x[i][1] * f, x[i][2] * f, x[i][3] * f),
+                               cvt4(x[i][4] * f, x[i][5] * f, x[i][6] * f, x[i][7] * f));
+    if (e0 + 8 <= a.cols) {
+      *reinterpret_cast<uint2*>(out) = q;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e0 + j < a.cols) out[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
+    if (l == 0) a.scales[(int64_t)kb[i] * a.ld_scales + row[i]] = m / kE4m3Max;
+  }
+}
+
+// Tiles of 128 rows x 128 columns, one per thread block, held in registers: a
+// thread has 8 columns of 8 rows (two groups of 4 consecutive ones), so that it
+// packs 4 codes of a column into a word for the transposed store.
+//   COLS   one scale per column of the tile, codes transposed [cols, rows]
+//   !COLS  one scale per tile; TRANS: codes transposed
+template <typename T, bool FAST, bool COLS, bool TRANS>
+__global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const QuantArgs a, const T* __restrict__ in0) {
+  pdl_wait();
+  __shared__ uint32_t words[TRANS ? kBlk * 33 : 1];  // [column][4-row group], one word of padding
+  __shared__ float part[8][COLS ? kBlk : 1];
+  __shared__ float factor[COLS ? kBlk : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = (int64_t)blockIdx.y * kBlk;
+  const int c0 = (int)blockIdx.x * kBlk;
+  const int64_t rows = a.rows_used ? min((int64_t)__ldg(a.rows_used), a.rows) : a.rows;
+  if (r0 >= rows) return;
+  const T* in = in0 + (int64_t)blockIdx.z * a.plane_in;
+  uint8_t* codes = a.codes + (int64_t)blockIdx.z * a.plane_codes;
+  float* scales = a.scales + (int64_t)blockIdx.z * a.plane_scales;
+  const int col = 8 * (lane & 15);
+  const int group = 2 * warp + (lane >> 4);  // rows 4 group .. + 3, and 64 more
+  float x[8][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + 4 * group + (i & 3) + 64 * (i >> 2);
+    int64_t from = r < rows ? r : -1;
+    if (from >= 0 && a.row_src) from = __ldg(a.row_src + r);
+    if (from >= 0) {
+      load8<T, FAST>(in + from * a.ld_in, c0 + col, a.cols, x[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+    }
+  }
+  float f[8];
+  if constexpr (COLS) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float m = kAmaxFloor;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i][j]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if (lane < 16) part[warp][col + j] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBlk) {
+      float m = part[0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) m = fmaxf(m, part[w][threadIdx.x]);
+      factor[threadIdx.x] = kE4m3Max / m;
+      if (c0 + (int)threadIdx.x < a.cols) scales[(int64_t)blockIdx.y * a.ld_scales + c0 + threadIdx.x] = m / kE4m3Max;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = factor[col + j];
+  } else {
+    float m = kAmaxFloor;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[i][j]));
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    if (lane == 0) part[warp][0] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = fmaxf(m, part[w][0]);
+    const float g = kE4m3Max / m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = g;
+    if (threadIdx.x == 0)
+      scales[TRANS ? (int64_t)blockIdx.x * a.ld_scales + blockIdx.y : (int64_t)blockIdx.y * a.ld_scales + blockIdx.x] =
+          m / kE4m3Max;
+  }
+  if constexpr (TRANS) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        words[(col + j) * 33 + group + 16 * h] = cvt4(x[4 * h][j] * f[j], x[4 * h + 1][j] * f[j],
+                                                      x[4 * h + 2][j] * f[j], x[4 * h + 3][j] * f[j]);
+    __syncthreads();
+    const int64_t r = r0 + 4 * lane;
+    for (int c = warp; c < kBlk && c0 + c < a.cols; c += 8) {
+      const uint32_t w = words[c * 33 + lane];
+      uint8_t* out = codes + (int64_t)(c0 + c) * a.ld_codes + r;
+      if (r + 4 <= rows) {
+        *reinterpret_cast<uint32_t*>(out) = w;
+      } else {
+        for (int b = 0; b < 4 && r + b < rows; ++b) out[b] = (uint8_t)(w >> (8 * b));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + 4 * group + (i & 3) + 64 * (i >> 2);
+      if (r >= rows) continue;
+      uint8_t* out = codes + r * a.ld_codes + c0 + col;
+      const uint2 q = make_uint2(cvt4(x[i][0] * f[0], x[i][1] * f[1], x[i][2] * f[2], x[i][3] * f[3]),
+                                 cvt4(x[i][4] * f[4], x[i][5] * f[5], x[i][6] * f[6], x[i][7] * f[7]));
+      if (c0 + col + 8 <= a.cols) {
+        *reinterpret_cast<uint2*>(out) = q;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c0 + col + j < a.cols) out[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_rows(const QuantArgs& a, const void* in, bool swiglu, cudaStream_t s) {
+  const unsigned grid = (unsigned)cdiv(a.rows * a.kblocks, 32);
+  const T* x = static_cast<const T*>(in);
+  const bool fast = fast_rows<T>(in, a.ld_in, a.cols);
+  if (swiglu)
+    return fast ? launch_pdl(fp8_quant_rows_kernel<T, true, true>, dim3(grid), dim3(256), 0, s, a, x)
+                : launch_pdl(fp8_quant_rows_kernel<T, false, true>, dim3(grid), dim3(256), 0, s, a, x);
+  return fast ? launch_pdl(fp8_quant_rows_kernel<T, true, false>, dim3(grid), dim3(256), 0, s, a, x)
+              : launch_pdl(fp8_quant_rows_kernel<T, false, false>, dim3(grid), dim3(256), 0, s, a, x);
+}
+
+template <typename T, bool COLS, bool TRANS>
+cudaError_t launch_tiles(const QuantArgs& a, int E, const void* in, cudaStream_t s) {
+  const dim3 grid((unsigned)cdiv(a.cols, kBlk), (unsigned)cdiv(a.rows, kBlk), (unsigned)E);
+  const T* x = static_cast<const T*>(in);
+  const bool fast = fast_rows<T>(in, a.ld_in, a.cols) && a.plane_in * (int64_t)sizeof(T) % 16 == 0;
+  return fast ? launch_pdl(fp8_quant_tile_kernel<T, true, COLS, TRANS>, grid, dim3(256), 0, s, a, x)
+              : launch_pdl(fp8_quant_tile_kernel<T, false, COLS, TRANS>, grid, dim3(256), 0, s, a, x);
+}
+
+int64_t elem_size(moe_dtype t) { return t == MOE_F32 ? 4 : (t == MOE_BF16 || t == MOE_F16) ? 2 : 0; }
+moe_status check_quant(moe_dtype type, const void* in, int64_t ld_in, int64_t width, const void* codes,
+                       int64_t ld_codes, int64_t code_cols, const float* scales) {
+  const int64_t es = elem_size(type);
+  if (es == 0) return MOE_ERR_INVALID_ARG;
+  if (!in || !codes || !scales || reinterpret_cast<uintptr_t>(in) % (uintptr_t)es || !aligned16(codes) ||
+      (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return MOE_ERR_INVALID_ARG;
+  if (ld_in < width || ld_codes < code_cols || ld_codes % 16 != 0) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+#define MOE_TRY_CUDA(...)                                                              \
+  do {                                                                                 \
+    const cudaError_t moe_e_ = (__VA_ARGS__);                                          \
+    if (moe_e_ != cudaSuccess) return api_cuda_failed(moe_e_, "moe_fp8.cu", __LINE__); \
+  } while (0)
+#define MOE_BY_TYPE(type, CALL)                                   \
+  switch (type) {                                                 \
+    case MOE_BF16: { using T = __nv_bfloat16; MOE_TRY_CUDA(CALL); break; } \
+    case MOE_F16: { using T = __half; MOE_TRY_CUDA(CALL); break; }         \
+    default: { using T = float; MOE_TRY_CUDA(CALL); }                      \
+  }
+
+extern "C" {
+
+moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
+                                 const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
+                                 int64_t ld_codes, float* scales, int64_t ld_scales, void* stream) {
+  ApiRange api_range("moe_fp8_quantize_rows");
+  if (rows < 0 || cols < 1 || swiglu < 0 || swiglu > 1) return MOE_ERR_INVALID_ARG;
+  const int kb = (int)cdiv(cols, kBlk);
+  if (cols > (1 << 20) || rows * kb >= (int64_t(1) << 32) - 32) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const moe_status st = check_quant(type, in, ld_in, (int64_t)cols * (1 + swiglu), codes, ld_codes, cols, scales);
+  if (st != MOE_OK) return st;
+  if (ld_scales < rows) return MOE_ERR_INVALID_ARG;
+  QuantArgs a = {};
+  a.rows = rows;
+  a.ld_in = ld_in;
+  a.ld_codes = ld_codes;
+  a.ld_scales = ld_scales;
+  a.cols = cols;
+  a.kblocks = kb;
+  a.row_src = row_src;
+  a.rows_used = rows_used;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps(s, "fp8_quantize_rows");
+  MOE_BY_TYPE(type, (launch_rows<T>(a, in, swiglu != 0, s)));
+  return MOE_OK;
+}
+
+moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
+                                 const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
+                                 float* scales, int64_t ld_scales, void* stream) {
+  ApiRange api_range("moe_fp8_quantize_cols");
+  if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
+  if (cols > (1 << 20) || cdiv(rows, kBlk) > 65535) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const moe_status st = check_quant(type, in, ld_in, cols, codes, ld_codes, rows, scales);
+  if (st != MOE_OK) return st;
+  if (ld_scales < cols) return MOE_ERR_INVALID_ARG;
+  QuantArgs a = {};
+  a.rows = rows;
+  a.ld_in = ld_in;
+  a.ld_codes = ld_codes;
+  a.ld_scales = ld_scales;
+  a.cols = cols;
+  a.row_src = row_src;
+  a.rows_used = rows_used;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps(s, "fp8_quantize_cols");
+  MOE_BY_TYPE(type, (launch_tiles<T, true, true>(a, 1, in, s)));
+  return MOE_OK;
+}
+
+moe_status moe_fp8_quantize_blocks(moe_dtype type, const void* in, int32_t E, int32_t K, int32_t N, int32_t transpose,
+                                   void* codes, int64_t ld_codes, float* scales, void* stream) {
+  ApiRange api_range("moe_fp8_quantize_blocks");
+  if (E < 0 || K < 1 || N < 1 || transpose < 0 || transpose > 1) return MOE_ERR_INVALID_ARG;
+  if (E > 65535 || K > 65535 * kBlk || N > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (E == 0) return MOE_OK;
+  const moe_status st = check_quant(type, in, N, N, codes, ld_codes, transpose ? K : N, scales);
+  if (st != MOE_OK) return st;
+  QuantArgs a = {};
+  a.rows = K;
+  a.ld_in = N;
+  a.ld_codes = ld_codes;
+  a.ld_scales = transpose ? cdiv(K, kBlk) : cdiv(N, kBlk);
+  a.cols = N;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  a.plane_in = (int64_t)K * N;
+  a.plane_codes = (int64_t)(transpose ? N : K) * ld_codes;
+  a.plane_scales = cdiv(K, kBlk) * cdiv(N, kBlk);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope ps(s, "fp8_quantize_blocks");
+  if (transpose) {
+    MOE_BY_TYPE(type, (launch_tiles<T, false, true>(a, E, in, s)));
+  } else {
+    MOE_BY_TYPE(type, (launch_tiles<T, false, false>(a, E, in, s)));
+  }
+  return MOE_OK;
+}
+
+// ----------------------------------------------------------------- products
+static moe_status fp8_product(int mode, int64_t M, int64_t N, int64_t K, int32_t planes, const moe_routing* rt,
+                              const void* A, int64_t lda, const float* sA, int64_t ldsA, const void* B, int64_t ldb,
+                              const float* sB, int64_t ldsB, void* C, int64_t ldc, cudaStream_t s) {
+  ApiDevice dev;
+  if (!api_device(&dev)) return MOE_ERR_CUDA;
+  Fp8Params p;
+  memset(&p, 0, sizeof(p));
+  const bool dw = mode == FP8_DW;
+  const uint64_t bplanes = mode == FP8_GROUPED ? planes : 1, cplanes = dw ? planes : 1;
+  if (!api_tensor_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, 1, M, K, lda, (uint64_t)M * lda, 128, 128) ||
+      !api_tensor_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, bplanes, N, K, ldb, (uint64_t)N * ldb, 128, 128) ||
+      !api_tensor_map(&p.tmC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C, cplanes, M, N, 2 * ldc, (uint64_t)M * 2 * ldc, 32, 64))
+    return MOE_ERR_INVALID_ARG;
+  p.sA = sA;
+  p.sB = sB;
+  p.ldsA = ldsA;
+  p.ldsB = ldsB;
+  p.ldc = ldc;
+  p.C = static_cast<__nv_bfloat16*>(C);
+  p.offsets = rt ? rt->offsets : nullptr;
+  p.tile_expert = rt ? rt->tile_expert : nullptr;
+  p.E = planes;
+  p.M = (int)M;
+  p.N = (int)N;
+  p.nb = (int)cdiv(N, 128);
+  p.kb = (int)cdiv(K, 128);
+  p.mode = mode;
+  p.mt = (int)cdiv(M, 128);
+  p.st = DevStatus{dev.status, dev.spin_limit};
+  constexpr int HALVES = 1;
+  p.nt = (int)cdiv(N, 128 * HALVES);
+  const int64_t tiles = (int64_t)p.mt * p.nt * cplanes;
+  if (tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  const int grid = (int)std::min<int64_t>(tiles, dev.sms);
+  using SH = Fp8Shape<HALVES>;
+  const void* fn = dw ? reinterpret_cast<const void*>(fp8_gemm_kernel<HALVES, true>)
+                      : reinterpret_cast<const void*>(fp8_gemm_kernel<HALVES, false>);
+  MOE_TRY_CUDA(set_max_dynamic_smem(fn, SH::kSmem));
+  ProfScope ps(s, dw ? "fp8_gemm_dw" : "fp8_gemm");
+  if (dw)
+    MOE_TRY_CUDA(launch_pdl(fp8_gemm_kernel<HALVES, true>, dim3(grid), dim3(SH::kThreads), SH::kSmem, s, p));
+  else
+    MOE_TRY_CUDA(launch_pdl(fp8_gemm_kernel<HALVES, false>, dim3(grid), dim3(SH::kThreads), SH::kSmem, s, p));
+  return MOE_OK;
+}
+
+static moe_status check_product(int64_t M, int64_t N, int64_t K, int32_t E, const moe_routing* rt, const void* A,
+                                int64_t lda, const float* sA, const void* B, int64_t ldb, const float* sB,
+                                const void* C, int64_t ldc) {
+  if (rt && (!rt->offsets || !rt->tile_expert || !aligned16(rt->offsets) || !aligned16(rt->tile_expert)))
+    return MOE_ERR_INVALID_ARG;
+  if (M >= (int64_t(1) << 31) - 256 || N >= (int64_t(1) << 31) - 256 || K >= (int64_t(1) << 31) - 256 || E > 1024 ||
+      (!rt && E != 1))
+    return MOE_ERR_UNSUPPORTED;
+  if (!A || !B || !C || !sA || !sB || !aligned16(A) || !aligned16(B) || !aligned16(C)) return MOE_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(sA) & 3u) || (reinterpret_cast<uintptr_t>(sB) & 3u)) return MOE_ERR_INVALID_ARG;
+  if (lda < K || ldb < K || ldc < N || lda % 16 || ldb % 16 || ldc % 8) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status moe_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t E, const moe_routing* rt, const void* A, int64_t lda,
+                        const float* sA, int64_t ldsA, const void* B, int64_t ldb, const float* sB, void* C,
+                        int64_t ldc, void* stream) {
+  ApiRange api_range("moe_fp8_gemm");
+  if (M < 0 || N < 1 || K < 1 || E < 1) return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  const moe_status st = check_product(M, N, K, E, rt, A, lda, sA, B, ldb, sB, C, ldc);
+  if (st != MOE_OK) return st;
+  if (ldsA < M || (rt && M % 128 != 0)) return MOE_ERR_INVALID_ARG;
+  return fp8_product(rt ? FP8_GROUPED : FP8_DENSE, M, N, K, E, rt, A, lda, sA, ldsA, B, ldb, sB, 0, C, ldc,
+                     static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_fp8_gemm_dw(int64_t M, int64_t N, int64_t K, int32_t E, const moe_routing* rt, const void* A,
+                           int64_t lda, const float* sA, int64_t ldsA, const void* B, int64_t ldb, const float* sB,
+                           int64_t ldsB, void* C, int64_t ldc, void* stream) {
+  ApiRange api_range("moe_fp8_gemm_dw");
+  if (M < 1 || N < 1 || K < 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (K == 0) {  // no tokens: no operands, a gradient of zeros
+    if (!C || !aligned16(C) || ldc < N || ldc % 8) return MOE_ERR_INVALID_ARG;
+    if (E > 1024) return MOE_ERR_UNSUPPORTED;
+    MOE_TRY_CUDA(cudaMemset2DAsync(C, (size_t)ldc * 2, 0, (size_t)N * 2, (size_t)(E * M), s));
+    return MOE_OK;
+  }
+  const moe_status st = check_product(M, N, K, E, rt, A, lda, sA, B, ldb, sB, C, ldc);
+  if (st != MOE_OK) return st;
+  if (ldsA < M || ldsB < N || (rt && K % 128 != 0)) return MOE_ERR_INVALID_ARG;
+  return fp8_product(FP8_DW, M, N, K, E, rt, A, lda, sA, ldsA, B, ldb, sB, ldsB, C, ldc, s);
+}
+
+}  // extern "C"

@@ -103,6 +103,16 @@ def lib() -> ctypes.CDLL:
         L.moe_unpermute.argtypes = L.moe_permute.argtypes
         L.moe_unpermute_bwd.argtypes = [c_int64, c_int32, c_int32, P(MoeRouting), c_int32, c_int64, c_void_p, c_int64,
                                         c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p]
+        L.moe_fp8_quantize_rows.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_void_p, c_int32,
+                                            c_void_p, c_int64, c_void_p, c_int64, c_void_p]
+        L.moe_fp8_quantize_cols.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_void_p, c_void_p,
+                                            c_int64, c_void_p, c_int64, c_void_p]
+        L.moe_fp8_quantize_blocks.argtypes = [c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
+                                              c_void_p, c_void_p]
+        L.moe_fp8_gemm.argtypes = [c_int64, c_int64, c_int64, c_int32, P(MoeRouting), c_void_p, c_int64, c_void_p,
+                                   c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p]
+        L.moe_fp8_gemm_dw.argtypes = [c_int64, c_int64, c_int64, c_int32, P(MoeRouting), c_void_p, c_int64, c_void_p,
+                                      c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
         L.moe_mx_quantize_rows.argtypes = [c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p]
         L.moe_mx_quantize_cols.argtypes = [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p]
         L.moe_get_status.argtypes = [c_void_p, P(c_int32)]
@@ -127,7 +137,8 @@ def lib() -> ctypes.CDLL:
                   "moe_set_sm_budget", "moe_mx_quantize_rows", "moe_mx_quantize_cols", "moe_forward_mxfp8",
                   "moe_route_given", "moe_ep_pack", "moe_ep_combine", "moe_router_backward",
                   "moe_mx_quantize_weights", "moe_forward_mxfp8_q", "moe_sort_sizes", "moe_sort_pairs", "moe_permute",
-                  "moe_permute_bwd", "moe_unpermute", "moe_unpermute_bwd"):
+                  "moe_permute_bwd", "moe_unpermute", "moe_unpermute_bwd", "moe_fp8_quantize_rows",
+                  "moe_fp8_quantize_cols", "moe_fp8_quantize_blocks", "moe_fp8_gemm", "moe_fp8_gemm_dw"):
             getattr(L, f).restype = c_int32
         _lib = L
     return _lib
@@ -491,6 +502,213 @@ def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: b
                                    ld, _ptr(drows), ldd, _ptr(dgate) if pairs else None,
                                    None if pairs else _ptr(dgate), _stream(stream)), "moe_unpermute_bwd")
     return drows, dgate
+
+
+# ----------------------------------------------------------------------------
+# 8-bit products with one fp32 scale per block of 128 (moe_fp8_* in moe.h).
+# Codes are float8_e4m3fn tensors whose rows are 16-byte aligned; those
+# allocated here have a row stride of the next multiple of 16.
+
+
+def _new_codes(lead, cols: int, device):
+    import torch
+    return torch.empty(*lead, (cols + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device=device)[..., :cols]
+
+
+def _codes(t, name: str, rows: int, cols: int, device) -> int:
+    import torch
+    ld = _matrix(t, name, rows, cols, device, torch.float8_e4m3fn)
+    if rows <= 1:
+        ld = (cols + 15) // 16 * 16
+    if ld % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must be 16-byte aligned (row stride {ld})")
+    return ld
+
+
+def _i32(t, name: str, n: int, device):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name}: {t.dtype}, expected torch.int32")
+    if t.device != device or t.dim() != 1 or t.shape[0] < n or (t.shape[0] > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: {n} contiguous values on {device} expected")
+    return _ptr(t)
+
+
+def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
+    import torch
+    code = _dtype_code(x, "x")
+    width = _width(x, "x")
+    dev = x.device
+    n_in = x.shape[0]
+    ld = _matrix(x, "x", n_in, width, dev)
+    if swiglu and width % 2:
+        raise ValueError(f"x: {width} columns, expected gate and up halves")
+    cols = width // 2 if swiglu else width
+    rows = n_in if row_src is None else row_src.shape[0]
+    src = _i32(row_src, "row_src", rows, dev)
+    used = _i32(rows_used, "rows_used", 1, dev)
+    if _away(dev):
+        return _on(dev, _quantize, cols_form, x, row_src, rows_used, swiglu, codes, scales, stream)
+    out, blocks = ((cols, rows), -(-rows // 128)) if cols_form else ((rows, cols), -(-cols // 128))
+    if codes is None:
+        codes = _new_codes(out[:1], out[1], dev)
+    if scales is None:
+        scales = torch.empty(blocks, out[0], dtype=torch.float32, device=dev)
+    ldc = _codes(codes, "codes", *out, dev)
+    lds = _matrix(scales, "scales", blocks, out[0], dev, torch.float32)
+    if cols_form:
+        _check(lib().moe_fp8_quantize_cols(code, _ptr(x), ld, rows, cols, src, used, _ptr(codes), ldc, _ptr(scales),
+                                           lds, _stream(stream)), "moe_fp8_quantize_cols")
+    else:
+        _check(lib().moe_fp8_quantize_rows(code, _ptr(x), ld, rows, cols, src, used, 1 if swiglu else 0, _ptr(codes),
+                                           ldc, _ptr(scales), lds, _stream(stream)), "moe_fp8_quantize_rows")
+    return codes, scales
+
+
+def fp8_quantize_rows(x, row_src=None, rows_used=None, swiglu: bool = False, codes=None, scales=None, stream=None):
+    """x [rows, cols] -> (codes [rows, cols], scales [ceil(cols / 128), rows]).
+    row_src [R] int32: row r of the result holds x[row_src[r]], zeros where it
+    is -1; its entries must be rows of x.  rows_used: a device int32; rows from
+    there on are left as they were.  swiglu: x is [rows, 2 cols] and
+    silu(x[:, :cols]) * x[:, cols:] is quantized."""
+    return _quantize(False, x, row_src, rows_used, swiglu, codes, scales, stream)
+
+
+def fp8_quantize_cols(x, row_src=None, rows_used=None, codes=None, scales=None, stream=None):
+    """x [rows, cols] -> (codes [cols, rows], scales [ceil(rows / 128), cols]):
+    one scale per column and 128 rows, codes transposed.  row_src and rows_used
+    as in fp8_quantize_rows."""
+    return _quantize(True, x, row_src, rows_used, False, codes, scales, stream)
+
+
+def fp8_quantize_blocks(w, transpose: bool, codes=None, scales=None, stream=None):
+    """w [E, K, N] or [K, N] (contiguous) -> codes and one scale per 128 x 128
+    block: [.., K, N] and [.., ceil(K/128), ceil(N/128)], or with transpose
+    [.., N, K] and [.., ceil(N/128), ceil(K/128)]."""
+    import torch
+    code = _dtype_code(w, "w")
+    if w.dim() not in (2, 3) or not w.is_contiguous():
+        raise ValueError(f"w: a contiguous [E, K, N] or [K, N] expected, got {tuple(w.shape)}")
+    dev = w.device
+    K, N = w.shape[-2:]
+    E = w.shape[0] if w.dim() == 3 else 1
+    if _away(dev):
+        return _on(dev, fp8_quantize_blocks, w, transpose, codes, scales, stream)
+    a, b = (N, K) if transpose else (K, N)
+    lead = w.shape[:-2]
+    if codes is None:
+        codes = _new_codes((*lead, a), b, dev)
+    if scales is None:
+        scales = torch.empty(*lead, -(-a // 128), -(-b // 128), dtype=torch.float32, device=dev)
+    ldc = _planes(codes, "codes", (*lead, a, b), dev)
+    if scales.shape != (*lead, -(-a // 128), -(-b // 128)) or not scales.is_contiguous() or scales.device != dev:
+        raise ValueError(f"scales: contiguous {(*lead, -(-a // 128), -(-b // 128))} on {dev} expected")
+    if scales.dtype != torch.float32:
+        raise TypeError(f"scales: {scales.dtype}, expected torch.float32")
+    _check(lib().moe_fp8_quantize_blocks(code, _ptr(w), E, K, N, 1 if transpose else 0, _ptr(codes), ldc, _ptr(scales),
+                                         _stream(stream)), "moe_fp8_quantize_blocks")
+    return codes, scales
+
+
+def _planes(t, name: str, shape, device) -> int:
+    """Check codes [rows, cols] or [E, rows, cols] without gaps between planes;
+    returns the row stride."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if len(shape) == 2:
+        return _codes(t, name, *shape, device)
+    if shape[0] == 0:
+        return (shape[2] + 15) // 16 * 16
+    ld = _codes(t[0], name, shape[1], shape[2], device)
+    if shape[0] > 1 and t.stride(0) != shape[1] * ld:
+        raise ValueError(f"{name}: planes must follow one another (stride {t.stride(0)}, expected {shape[1] * ld})")
+    return ld
+
+
+def _out(out, name, shape, device):
+    """bf16 result [.., rows, cols], its rows 16-byte aligned; returns (tensor, row stride)."""
+    import torch
+    if out is None:
+        ld = (shape[-1] + 7) // 8 * 8
+        return torch.empty(*shape[:-1], ld, dtype=torch.bfloat16, device=device)[..., :shape[-1]], ld
+    if out.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(out.shape)}, expected {tuple(shape)}")
+    flat = out if len(shape) == 2 else out[0]
+    ld = _matrix(flat, name, shape[-2], shape[-1], device, torch.bfloat16)
+    if shape[-2] <= 1:
+        ld = (shape[-1] + 7) // 8 * 8
+    if ld % 8 or out.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must be 16-byte aligned (row stride {ld})")
+    if len(shape) == 3 and shape[0] > 1 and out.stride(0) != shape[1] * ld:
+        raise ValueError(f"{name}: planes must follow one another")
+    return out, ld
+
+
+def fp8_gemm(a, sa, b, sb, routing: Routing | None = None, out=None, stream=None):
+    """out [M, N] bf16 = a [M, K] times b [N, K] transposed, codes with their
+    scales sa [ceil(K/128), M] and sb [ceil(N/128), ceil(K/128)].  With a
+    routing: a [R_max, K] in expert order, b [E, N, K], sb [E, .., ..]; rows
+    past the last segment are left as they were (undefined in a new tensor)."""
+    import torch
+    dev = a.device
+    K = _width(a, "a")
+    M = a.shape[0]
+    lda = _codes(a, "a", M, K, dev)
+    if routing is None:
+        E, lead = 1, ()
+    else:
+        _, E, R, rdev = _routed(routing)
+        lead = (E,)
+        if M != R or rdev != dev:
+            raise ValueError(f"a: {M} rows on {dev}, expected the routing's {R} on {rdev}")
+    if b.dim() != 2 + len(lead):
+        raise ValueError(f"b: shape {tuple(b.shape)}, expected {'[E, N, K]' if lead else '[N, K]'}")
+    N = b.shape[-2]
+    ldb = _planes(b, "b", (*lead, N, K), dev)
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    lds = _matrix(sa, "sa", kb, M, dev, torch.float32)
+    if sb.shape != (*lead, nb, kb) or sb.device != dev or not sb.is_contiguous():
+        raise ValueError(f"sb: contiguous {(*lead, nb, kb)} on {dev} expected, got {tuple(sb.shape)}")
+    if sb.dtype != torch.float32:
+        raise TypeError(f"sb: {sb.dtype}, expected torch.float32")
+    if _away(dev):
+        return _on(dev, fp8_gemm, a, sa, b, sb, routing, out, stream)
+    out, ldo = _out(out, "out", (M, N), dev)
+    _check(lib().moe_fp8_gemm(M, N, K, E, None if routing is None else ctypes.byref(routing.struct), _ptr(a), lda,
+                              _ptr(sa), lds, _ptr(b), ldb, _ptr(sb), _ptr(out), ldo, _stream(stream)), "moe_fp8_gemm")
+    return out
+
+
+def fp8_gemm_dw(a, sa, b, sb, routing: Routing | None = None, out=None, stream=None):
+    """Weight gradient out [M, N] bf16 = a [M, tokens] times b [N, tokens]
+    transposed, both as fp8_quantize_cols leaves them (sa [ceil(tokens/128), M],
+    sb [.., N]).  With a routing the tokens are its rows and out is [E, M, N],
+    each expert's product over its own rows."""
+    import torch
+    dev = a.device
+    K = _width(a, "a")
+    _width(b, "b")
+    M, N = a.shape[0], b.shape[0]
+    lda, ldb = _codes(a, "a", M, K, dev), _codes(b, "b", N, K, dev)
+    kb = (K + 127) // 128
+    ldsa = _matrix(sa, "sa", kb, M, dev, torch.float32)
+    ldsb = _matrix(sb, "sb", kb, N, dev, torch.float32)
+    if routing is None:
+        E, lead = 1, ()
+    else:
+        _, E, R, rdev = _routed(routing)
+        lead = (E,)
+        if K != R or rdev != dev:
+            raise ValueError(f"a: {K} tokens on {dev}, expected the routing's {R} rows on {rdev}")
+    if _away(dev):
+        return _on(dev, fp8_gemm_dw, a, sa, b, sb, routing, out, stream)
+    out, ldo = _out(out, "out", (*lead, M, N), dev)
+    _check(lib().moe_fp8_gemm_dw(M, N, K, E, None if routing is None else ctypes.byref(routing.struct), _ptr(a), lda,
+                                 _ptr(sa), ldsa, _ptr(b), ldb, _ptr(sb), ldsb, _ptr(out), ldo, _stream(stream)),
+           "moe_fp8_gemm_dw")
+    return out
 
 
 def moe_set_sm_budget(sms: int):

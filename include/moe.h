@@ -378,6 +378,67 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
                              const void* dout, int64_t ld_dout, const void* rows, int64_t ld_rows, void* drows,
                              int64_t ld_drows, float* pair_dgate, float* topk_dgate, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit products with one fp32 scale per block of 128: E4M3 codes, value =
+ * code * scale.  For a block whose largest magnitude is m (at least 2^-110):
+ * scale = m / 448, code = e4m3(x * (448 / m)), in fp32, rounded to nearest
+ * even; no code saturates.  A NaN gives the NaN code; a block that holds an
+ * infinity gets an infinite scale, so that its products are NaN.
+ *
+ * Layouts.  codes: [.., ld_codes] bytes, rows 16-byte aligned (base, and
+ * ld_codes a multiple of 16); bytes between a row's end and ld_codes are not
+ * written.  Input tensors need only be aligned to their elements.
+ *
+ * moe_fp8_quantize_rows: in[rows, cols] (rows ld_in elements apart) -> codes
+ *   [rows, ld_codes], scales[ceil(cols / 128), ld_scales] (ld_scales >= rows):
+ *   one per row and 128 columns.  row_src (nullable, [rows]): row r holds
+ *   in[row_src[r]], zeros where it is -1 (a routing's row_tok gathers the
+ *   tokens into expert order).  rows_used (nullable, one device int): rows from
+ *   *rows_used on are left as they were (a routing's offsets + E).  swiglu = 1:
+ *   in[.., 2 cols], and silu(in[c]) * in[cols + c] is quantized.
+ * moe_fp8_quantize_cols: the same input -> codes[cols, ld_codes] transposed
+ *   (ld_codes >= rows), scales[ceil(rows / 128), ld_scales] (ld_scales >= cols):
+ *   one per column and 128 rows, for products summed over the rows.
+ * moe_fp8_quantize_blocks: expert weights in[E, K, N] (contiguous), one scale
+ *   per 128 x 128 block.  transpose = 0: codes[E, K, ld_codes],
+ *   scales[E, ceil(K/128), ceil(N/128)]; 1: codes[E, N, ld_codes],
+ *   scales[E, ceil(N/128), ceil(K/128)].
+ */
+moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
+                                 const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
+                                 int64_t ld_codes, float* scales, int64_t ld_scales, void* stream);
+moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
+                                 const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
+                                 float* scales, int64_t ld_scales, void* stream);
+moe_status moe_fp8_quantize_blocks(moe_dtype type, const void* in, int32_t E, int32_t K, int32_t N, int32_t transpose,
+                                   void* codes, int64_t ld_codes, float* scales, void* stream);
+
+/*
+ * C[m, n] = sum over blocks b of 128 k of sA[b, m] sB[n / 128, b] (A_b[m] . B_b[n]),
+ * summed in fp32, C in bf16.  A[M, lda] and B codes with K contiguous; scales as
+ * the quantizers leave them: sA[ceil(K/128), ldsA], sB[E, ceil(N/128), ceil(K/128)].
+ *   rt NULL: one product, E = 1, B[N, ldb], C[M, ldc].
+ *   rt set: the rows of expert e (offsets[e] .. offsets[e + 1]) times B[e],
+ *     B[E, N, ldb] without gaps; M = the rows' capacity (a multiple of 128; the
+ *     routing's R_max).  Rows of C from offsets[E] on are left as they were;
+ *     padding rows are computed like any other (0 from codes of 0).
+ *   Y = X W with W[K, N] takes B quantized with transpose = 1, its input
+ *   gradient dX = dY W^T takes B quantized with transpose = 0.
+ * moe_fp8_gemm_dw: the weight gradient, both operands with a scale per row and
+ *   block of 128 tokens (moe_fp8_quantize_cols): C[m, n] = sum over blocks of
+ *   sA[b, m] sB[b, n] (A_b[m] . B_b[n]).  rt NULL: one product over K tokens,
+ *   C[M, ldc]; rt set: C[E, M, ldc], C[e] summed over expert e's rows, zeros
+ *   for an expert without rows; K = the rows' capacity (a multiple of 128).
+ * lda, ldb multiples of 16, ldc of 8; any M, N, K (no multiple needed); M = 0
+ * (moe_fp8_gemm) or K = 0 (moe_fp8_gemm_dw) are valid.
+ */
+moe_status moe_fp8_gemm(int64_t M, int64_t N, int64_t K, int32_t E, const moe_routing* rt, const void* A, int64_t lda,
+                        const float* sA, int64_t ldsA, const void* B, int64_t ldb, const float* sB, void* C,
+                        int64_t ldc, void* stream);
+moe_status moe_fp8_gemm_dw(int64_t M, int64_t N, int64_t K, int32_t E, const moe_routing* rt, const void* A,
+                           int64_t lda, const float* sA, int64_t ldsA, const void* B, int64_t ldb, const float* sB,
+                           int64_t ldsB, void* C, int64_t ldc, void* stream);
+
 /*
  * Synchronises `stream`, returns the device status word (MOE_OK if no kernel
  * reported an error since the last call) and clears it.  *where (nullable)
