@@ -376,6 +376,26 @@ moe_status moe_fp8_quantize_blocks(moe_dtype type, const void* in, int32_t E, in
 }
 
 // ----------------------------------------------------------------- products
+// Launch with a cluster of `split` CTAs and programmatic stream serialization.
+static cudaError_t launch_small(const Fp8Params& p, int grid, int smem, cudaStream_t s) {
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(fp8_gemm_small_kernel), 227 * 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(Fp8SmallShape::kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = MOE_PDL;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = p.split;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = p.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&c, fp8_gemm_small_kernel, p);
+}
+
 static moe_status fp8_product(int mode, int64_t M, int64_t N, int64_t K, int32_t planes, const moe_routing* rt,
                               const void* A, int64_t lda, const float* sA, int64_t ldsA, const void* B, int64_t ldb,
                               const float* sB, int64_t ldsB, void* C, int64_t ldc, cudaStream_t s) {
@@ -384,11 +404,6 @@ static moe_status fp8_product(int mode, int64_t M, int64_t N, int64_t K, int32_t
   Fp8Params p;
   memset(&p, 0, sizeof(p));
   const bool dw = mode == FP8_DW;
-  const uint64_t bplanes = mode == FP8_GROUPED ? planes : 1, cplanes = dw ? planes : 1;
-  if (!api_tensor_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, 1, M, K, lda, (uint64_t)M * lda, 128, 128) ||
-      !api_tensor_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, bplanes, N, K, ldb, (uint64_t)N * ldb, 128, 128) ||
-      !api_tensor_map(&p.tmC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C, cplanes, M, N, 2 * ldc, (uint64_t)M * 2 * ldc, 32, 64))
-    return MOE_ERR_INVALID_ARG;
   p.sA = sA;
   p.sB = sB;
   p.ldsA = ldsA;
@@ -403,22 +418,51 @@ static moe_status fp8_product(int mode, int64_t M, int64_t N, int64_t K, int32_t
   p.nb = (int)cdiv(N, 128);
   p.kb = (int)cdiv(K, 128);
   p.mode = mode;
-  p.mt = (int)cdiv(M, 128);
   p.st = DevStatus{dev.status, dev.spin_limit};
-  constexpr int HALVES = 1;
-  p.nt = (int)cdiv(N, 128 * HALVES);
-  const int64_t tiles = (int64_t)p.mt * p.nt * cplanes;
+  const uint64_t bplanes = mode == FP8_GROUPED ? planes : 1, cplanes = dw ? planes : 1;
+  const uint64_t bplane = (uint64_t)N * ldb;
+  // Pair tiles where they fill the machine, else tiles of 128 columns with the
+  // operands exchanged, of which the machine holds twice as many and which may
+  // share their sums (microseconds, pair tiles / exchanged: 16 x 4096 x 7168 28 /
+  // 13; 256 x 4096 x 7168, 16 pair tiles, 33 / 20; 1001 x 1528 x 2000, 24 pair
+  // tiles, 12.7 / 11.3; 2048 x 2048 x 2048, 64, 13 / 19).  Grouped products always
+  // take pairs: even with a few rows per expert they read the weights faster
+  // (64 tokens x 8 of 128 experts, 1536 x 2048: 118 / 133).
+  const bool few = mode == FP8_DENSE && cdiv(M, 256) * cdiv(N, 256) < dev.sms / 4;
+  if (few) {
+    p.tok_boxes = (int)std::min<int64_t>(4, cdiv(M, 32));
+    if (!api_tensor_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, bplanes, N, K, ldb, bplane, 128, 128) ||
+        !api_tensor_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, 1, M, K, lda, (uint64_t)M * lda, 32 * p.tok_boxes, 128))
+      return MOE_ERR_INVALID_ARG;
+    p.mt = (int)cdiv(M, 32 * p.tok_boxes);
+    p.nt = p.nb;
+    const int64_t tiles = (int64_t)p.mt * p.nt;
+    if (tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    p.split = 1;
+    while (p.split < 8 && 2 * tiles * p.split <= dev.sms && p.kb >= 4 * p.split) p.split *= 2;
+    const int grid = p.split > 1 ? (int)tiles * p.split : (int)std::min<int64_t>(tiles, dev.sms);
+    ProfScope ps(s, "fp8_gemm");
+    MOE_TRY_CUDA(launch_small(p, grid, Fp8SmallShape::smem(p.tok_boxes), s));
+    return MOE_OK;
+  }
+  if (!api_tensor_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, 1, M, K, lda, (uint64_t)M * lda, 128, 128) ||
+      !api_tensor_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, bplanes, N, K, ldb, bplane, 128, 128) ||
+      !api_tensor_map(&p.tmC, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, C, cplanes, M, N, 2 * ldc, (uint64_t)M * 2 * ldc, 32, 64))
+    return MOE_ERR_INVALID_ARG;
+  p.mt = (int)cdiv(M, 256);
+  p.nt = (int)cdiv(N, 256);
+  // GROUPED: an expert's odd last tile is a pair tile too
+  const int64_t tiles = ((int64_t)p.mt + (mode == FP8_GROUPED ? planes : 0)) * p.nt * cplanes;
   if (tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
-  const int grid = (int)std::min<int64_t>(tiles, dev.sms);
-  using SH = Fp8Shape<HALVES>;
-  const void* fn = dw ? reinterpret_cast<const void*>(fp8_gemm_kernel<HALVES, true>)
-                      : reinterpret_cast<const void*>(fp8_gemm_kernel<HALVES, false>);
+  using SH = Fp8PairShape;
+  const void* fn = dw ? reinterpret_cast<const void*>(fp8_gemm_pair_kernel<true>)
+                      : reinterpret_cast<const void*>(fp8_gemm_pair_kernel<false>);
   MOE_TRY_CUDA(set_max_dynamic_smem(fn, SH::kSmem));
+  const int most = std::max(1, std::min(dev.sms / 2, resident_pairs(fn, SH::kThreads, SH::kSmem)));
+  const int pairs = (int)std::min<int64_t>(tiles, most);
   ProfScope ps(s, dw ? "fp8_gemm_dw" : "fp8_gemm");
-  if (dw)
-    MOE_TRY_CUDA(launch_pdl(fp8_gemm_kernel<HALVES, true>, dim3(grid), dim3(SH::kThreads), SH::kSmem, s, p));
-  else
-    MOE_TRY_CUDA(launch_pdl(fp8_gemm_kernel<HALVES, false>, dim3(grid), dim3(SH::kThreads), SH::kSmem, s, p));
+  MOE_TRY_CUDA(dw ? launch_pdl(fp8_gemm_pair_kernel<true>, dim3(2 * pairs), dim3(SH::kThreads), SH::kSmem, s, p)
+                  : launch_pdl(fp8_gemm_pair_kernel<false>, dim3(2 * pairs), dim3(SH::kThreads), SH::kSmem, s, p));
   return MOE_OK;
 }
 

@@ -65,7 +65,7 @@ static cudaError_t launch_pair_one(const GemmParams& p, int pairs, cudaStream_t 
 // device (one CTA per SM; a cluster needs two SMs of one GPC), once per
 // (function, device).  A persistent pair kernel launches no more, so that no
 // pair waits for another to finish before it starts its share of the tiles.
-static int resident_pairs(const void* fn, int threads, int smem) {
+int resident_pairs(const void* fn, int threads, int smem) {
   static std::mutex mu;
   static std::map<std::pair<const void*, int>, int> known;
   int dev = 0;

@@ -43,6 +43,9 @@ constexpr int kChunk = 256;       // tokens per ranking chunk of the permutation
 // (function, device); thread-safe.
 cudaError_t set_max_dynamic_smem(const void* fn, int bytes);
 
+// Pairs of a 2-CTA cluster kernel that can be resident at once on the current device.
+int resident_pairs(const void* fn, int threads, int smem);
+
 // Role timeline of GEMM kind `kind` (GemmKind) into `buf` (null: off), `cap`
 // records per CTA and role.
 void set_gemm_trace(int kind, void* buf, int cap);

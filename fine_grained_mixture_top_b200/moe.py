@@ -165,7 +165,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int:
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without the Python object around it (0.1 instead of 3.4 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -512,7 +513,9 @@ def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: b
 
 def _new_codes(lead, cols: int, device):
     import torch
-    return torch.empty(*lead, (cols + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device=device)[..., :cols]
+    ld = (cols + 15) // 16 * 16
+    codes = torch.empty(*lead, ld, dtype=torch.float8_e4m3fn, device=device)
+    return codes if ld == cols else codes[..., :cols]
 
 
 def _codes(t, name: str, rows: int, cols: int, device) -> int:
@@ -632,7 +635,8 @@ def _out(out, name, shape, device):
     import torch
     if out is None:
         ld = (shape[-1] + 7) // 8 * 8
-        return torch.empty(*shape[:-1], ld, dtype=torch.bfloat16, device=device)[..., :shape[-1]], ld
+        out = torch.empty(*shape[:-1], ld, dtype=torch.bfloat16, device=device)
+        return out if ld == shape[-1] else out[..., :shape[-1]], ld
     if out.shape != shape:
         raise ValueError(f"{name}: shape {tuple(out.shape)}, expected {tuple(shape)}")
     flat = out if len(shape) == 2 else out[0]
