@@ -10,7 +10,6 @@
 // value: bound by those bytes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -30,37 +29,100 @@ constexpr int kBlk = 128;  // values per scale
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 7.7037197775489434e-34f;  // 2^-110
 
-__device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+// Four values to four E4M3 codes (rounded to nearest even, saturating), the first
+// in the lowest byte.
+__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
-__device__ __forceinline__ uint32_t cvt4(float a, float b, float c, float d) { return cvt2(a, b) | cvt2(c, d) << 16; }
-
-// Eight values of a row from element e0 on (a multiple of 8), zeros outside
-// [0, width).  FAST: the row's 16-byte pieces are aligned and width is a
-// multiple of 8.  Otherwise pieces whose windows stay inside the row come from
-// two windows each, and those at its ends element by element.
-template <typename T, bool FAST>
-__device__ __forceinline__ void load8(const T* row, int e0, int width, float (&x)[8]) {
-  constexpr int V = kVec<T>;
-  if (FAST ? e0 < width : (e0 >= V - 1 && e0 + 8 + V - 1 <= width)) {
-    Piece<T> p[8 / V];
+// x *= f, two values per instruction
+__device__ __forceinline__ void mul8(float (&x)[8], float f) {
+  uint64_t ff;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ff) : "f"(f));
 #pragma unroll
-    for (int i = 0; i < 8 / V; ++i) p[i] = load_piece<T, FAST>(row + e0 + i * V);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_float(p[i / V].x[i % V]);
-    return;
+  for (int i = 0; i < 4; ++i) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x[2 * i]), "f"(x[2 * i + 1]));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(ff));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x[2 * i]), "=f"(x[2 * i + 1]) : "l"(v));
   }
+}
+
+// Eight values of a row as they are stored, from element e0 on (a multiple of
+// 8), zeros outside [0, width).  FAST: the row's 16-byte pieces are aligned and
+// width is a multiple of 8.  Otherwise pieces whose windows stay inside the row
+// come from two windows each, and those at its ends element by element.
+template <typename T>
+struct Raw8 {
+  Piece<T> p[8 / kVec<T>];
+  __device__ __forceinline__ float operator[](int i) const { return to_float(p[i / kVec<T>].x[i % kVec<T>]); }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = !FAST && e0 + i < width ? to_float(row[e0 + i]) : 0.f;
+    for (int i = 0; i < 8 / kVec<T>; ++i) *reinterpret_cast<uint4*>(&p[i]) = make_uint4(0u, 0u, 0u, 0u);
+  }
+};
+template <typename T, bool FAST>
+__device__ __forceinline__ Raw8<T> load8(const T* row, int e0, int width) {
+  constexpr int V = kVec<T>;
+  Raw8<T> r;
+  if (FAST ? e0 < width : (e0 >= V - 1 && e0 + 8 + V - 1 <= width)) {
+#pragma unroll
+    for (int i = 0; i < 8 / V; ++i) r.p[i] = load_piece<T, FAST>(row + e0 + i * V);
+    return r;
+  }
+  r.clear();
+  if constexpr (!FAST) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e0 + i < width) r.p[i / V].x[i % V] = row[e0 + i];
+  }
+  return r;
+}
+// Largest magnitude among them (a NaN does not count); 16-bit types two at a time.
+__device__ __forceinline__ float amax8(const Raw8<float>& r) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(r[i]));
+  return m;
+}
+__device__ __forceinline__ float amax8(const Raw8<__nv_bfloat16>& r) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r.p[0]);
+  const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float amax8(const Raw8<__half>& r) {
+  const __half2* h = reinterpret_cast<const __half2*>(&r.p[0]);
+  const __half2 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+  return fmaxf(__low2float(m), __high2float(m));
 }
 template <typename T>
 bool fast_rows(const void* in, int64_t ld, int64_t width) {
   return aligned16(in) && ld * (int64_t)sizeof(T) % 16 == 0 && width % 8 == 0;
 }
 
+// n / d for n < 2^31 by a product: mul = ceil(2^(31 + s) / d), 2^(s - 1) < d <= 2^s.
+struct FastDiv {
+  uint32_t mul, shift, d;
+  explicit FastDiv(uint32_t d_ = 1) : mul(0), shift(0), d(d_) {
+    if (d < 2) return;
+    uint32_t s = 1;
+    while ((1u << s) < d) ++s;
+    mul = (uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d);
+    shift = s - 1;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return d < 2 ? n : __umulhi(n, mul) >> shift; }
+};
+
 struct QuantArgs {
   int64_t rows, ld_in, ld_codes, ld_scales;
   int cols, kblocks;           // blocks of a row (rows kernel)
+  FastDiv by_kblocks;
   const int* row_src;          // nullable: the input row of each row, -1: zeros
   const int* rows_used;        // nullable: rows from here on are left as they are
   uint8_t* codes;
@@ -70,66 +132,108 @@ struct QuantArgs {
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
-// Rows: a block of 128 values per half warp, 8 per lane; each thread has two
-// blocks, 16 apart in a thread block's run of 32, in flight at once.
-template <typename T, bool FAST, bool SWIGLU>
-__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const QuantArgs a, const T* __restrict__ in) {
-  pdl_wait();
-  const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int64_t used = a.rows_used ? min((int64_t)__ldg(a.rows_used), a.rows) : a.rows;
-  float x[2][8];
-  int64_t row[2];
-  int kb[2];
-  bool live[2];
+// eight codes from column e0 on, clipped to `cols`
+__device__ __forceinline__ void store_codes(uint8_t* out, const float (&x)[8], int e0, int cols) {
+  const uint2 q = make_uint2(cvt4(x[0], x[1], x[2], x[3]), cvt4(x[4], x[5], x[6], x[7]));
+  if (e0 + 8 <= cols) {
+    *reinterpret_cast<uint2*>(out) = q;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t unit = blockIdx.x * 32u + i * 16u + half;
-    const uint32_t r = unit / (uint32_t)a.kblocks;
-    row[i] = r;
-    kb[i] = (int)(unit - r * (uint32_t)a.kblocks);
-    live[i] = row[i] < used;
-    int64_t from = row[i];
-    if (live[i] && a.row_src) from = __ldg(a.row_src + row[i]);
-    const int e0 = kb[i] * kBlk + 8 * l;
-    if (live[i] && from >= 0) {
-      const T* src = in + from * a.ld_in;
-      load8<T, FAST>(src, e0, a.cols, x[i]);
-      if constexpr (SWIGLU) {  // up projection behind the gate's `cols` columns
-        float u[8];
-        load8<T, FAST>(src + a.cols, e0, a.cols, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i][j] = silu_mul(x[i][j], u[j]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float m = kAmaxFloor;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[i][j]));
-#pragma unroll
-    for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    if (!live[i]) continue;
-    const float f = kE4m3Max / m;
-    const int e0 = kb[i] * kBlk + 8 * l;
-    uint8_t* out = a.codes + row[i] * a.ld_codes + e0;
-    const uint2 q = make_uint2(cvt4(x[i][0] * f, x[i][1] * f, x[i][2] * f, x[i][3] * f),
-                               cvt4(x[i][4] * f, x[i][5] * f, x[i][6] * f, x[i][7] * f));
-    if (e0 + 8 <= a.cols) {
-      *reinterpret_cast<uint2*>(out) = q;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e0 + j < a.cols) out[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-    }
-    if (l == 0) a.scales[(int64_t)kb[i] * a.ld_scales + row[i]] = m / kE4m3Max;
+    for (int j = 0; j < 8; ++j)
+      if (e0 + j < cols) out[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
   }
 }
 
-// Tiles of 128 rows x 128 columns, one per thread block, held in registers: a
+// Sixteen values from element e0 on (a multiple of 16).  LOAD: 0 any alignment, 1
+// as load8's FAST, 2 the row's 32-byte pieces are aligned and width is a multiple
+// of 16.
+template <typename T, int LOAD>
+__device__ __forceinline__ void load16_values(Raw8<T> (&x)[2], const T* row, int e0, int width) {
+  if constexpr (LOAD == 2) {
+    if (e0 >= width) {
+      x[0].clear();
+      x[1].clear();
+      return;
+    }
+    constexpr int N = 8 / kVec<T>;  // 16-byte pieces per Raw8
+    uint4 u[2 * N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) load32(row + e0 + i * 2 * kVec<T>, u[2 * i], u[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) *reinterpret_cast<uint4*>(&x[i / N].p[i % N]) = u[i];
+  } else {
+    x[0] = load8<T, LOAD == 1>(row, e0, width);
+    x[1] = load8<T, LOAD == 1>(row, e0 + 8, width);
+  }
+}
+
+// Rows: a block of 128 values per 4 lanes, 32 per lane in two runs of 16, 64
+// apart, so that 4 lanes read 128 bytes of a 16-bit type and write 64 at a time.
+// At memory's rate the kernel has some 16 instructions and 1/12 of a shared
+// L1 wavefront per value.  With 8 values per lane and scalar maxima it was bound
+// by issue (182 us), with 32 in runs of 8 by L1 wavefronts (120 us); it now takes
+// 110 us (16384 tokens of 2048 bf16 values gathered 8 times).
+template <typename T, int LOAD, bool SWIGLU>
+__global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const QuantArgs a, const T* __restrict__ in) {
+  pdl_wait();
+  const int l = threadIdx.x & 3;
+  const uint32_t unit = blockIdx.x * 64u + (threadIdx.x >> 2);
+  const uint32_t row = a.by_kblocks.div(unit);
+  const int kb = (int)(unit - row * (uint32_t)a.kblocks);
+  const int64_t used = a.rows_used ? min((int64_t)__ldg(a.rows_used), a.rows) : a.rows;
+  const bool live = row < used;
+  const int64_t from = live ? (a.row_src ? (int64_t)__ldg(a.row_src + row) : (int64_t)row) : -1;
+  const int e0 = kb * kBlk + 16 * l;
+  const int width = from < 0 ? 0 : a.cols;  // nothing to load: zeros
+  const T* src = in + (from < 0 ? 0 : from) * a.ld_in;
+  Raw8<T> x[2][2];
+  float v[SWIGLU ? 4 : 1][8];
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load16_values<T, LOAD>(x[i], src, e0 + 64 * i, width);
+  if constexpr (SWIGLU) {  // the up projection lies behind the gate's `cols` columns
+    Raw8<T> up[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load16_values<T, LOAD>(up[i], src + a.cols, e0 + 64 * i, width);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = silu_mul(x[i >> 1][i & 1][j], up[i >> 1][i & 1][j]);
+        m = fmaxf(m, fabsf(v[i][j]));
+      }
+  } else {
+    m = fmaxf(fmaxf(amax8(x[0][0]), amax8(x[0][1])), fmaxf(amax8(x[1][0]), amax8(x[1][1])));
+  }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, kAmaxFloor);
+  if (!live) return;
+  const float f = kE4m3Max / m;
+  uint8_t* out = a.codes + (int64_t)row * a.ld_codes + e0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float w[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[h][j] = SWIGLU ? v[SWIGLU ? 2 * i + h : 0][j] : x[i][h][j];
+    mul8(w[0], f);
+    mul8(w[1], f);
+    if (e0 + 64 * i + 16 <= a.cols) {
+      *reinterpret_cast<uint4*>(out + 64 * i) =
+          make_uint4(cvt4(w[0][0], w[0][1], w[0][2], w[0][3]), cvt4(w[0][4], w[0][5], w[0][6], w[0][7]),
+                     cvt4(w[1][0], w[1][1], w[1][2], w[1][3]), cvt4(w[1][4], w[1][5], w[1][6], w[1][7]));
+    } else {
+      store_codes(out + 64 * i, w[0], e0 + 64 * i, a.cols);
+      store_codes(out + 64 * i + 8, w[1], e0 + 64 * i + 8, a.cols);
+    }
+  }
+  if (l == 0) a.scales[(int64_t)kb * a.ld_scales + row] = m / kE4m3Max;
+}
+
+// Tiles of 128 rows x 128 columns, one per thread block, held in registers as they
+// are stored (which leaves room for more thread blocks than fp32 would): a
 // thread has 8 columns of 8 rows (two groups of 4 consecutive ones), so that it
 // packs 4 codes of a column into a word for the transposed store.
 //   COLS   one scale per column of the tile, codes transposed [cols, rows]
@@ -150,18 +254,14 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const QuantArgs a, 
   float* scales = a.scales + (int64_t)blockIdx.z * a.plane_scales;
   const int col = 8 * (lane & 15);
   const int group = 2 * warp + (lane >> 4);  // rows 4 group .. + 3, and 64 more
-  float x[8][8];
+  Raw8<T> x[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 4 * group + (i & 3) + 64 * (i >> 2);
     int64_t from = r < rows ? r : -1;
     if (from >= 0 && a.row_src) from = __ldg(a.row_src + r);
-    if (from >= 0) {
-      load8<T, FAST>(in + from * a.ld_in, c0 + col, a.cols, x[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-    }
+    if (from >= 0) x[i] = load8<T, FAST>(in + from * a.ld_in, c0 + col, a.cols);
+    else x[i].clear();
   }
   float f[8];
   if constexpr (COLS) {
@@ -187,9 +287,7 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const QuantArgs a, 
   } else {
     float m = kAmaxFloor;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[i][j]));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, amax8(x[i]));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
     if (lane == 0) part[warp][0] = m;
@@ -226,30 +324,27 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const QuantArgs a, 
     for (int i = 0; i < 8; ++i) {
       const int64_t r = r0 + 4 * group + (i & 3) + 64 * (i >> 2);
       if (r >= rows) continue;
-      uint8_t* out = codes + r * a.ld_codes + c0 + col;
-      const uint2 q = make_uint2(cvt4(x[i][0] * f[0], x[i][1] * f[1], x[i][2] * f[2], x[i][3] * f[3]),
-                                 cvt4(x[i][4] * f[4], x[i][5] * f[5], x[i][6] * f[6], x[i][7] * f[7]));
-      if (c0 + col + 8 <= a.cols) {
-        *reinterpret_cast<uint2*>(out) = q;
-      } else {
+      float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c0 + col + j < a.cols) out[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-      }
+      for (int j = 0; j < 8; ++j) v[j] = x[i][j] * f[j];
+      store_codes(codes + r * a.ld_codes + c0 + col, v, c0 + col, a.cols);
     }
   }
 }
 
 template <typename T>
 cudaError_t launch_rows(const QuantArgs& a, const void* in, bool swiglu, cudaStream_t s) {
-  const unsigned grid = (unsigned)cdiv(a.rows * a.kblocks, 32);
+  const unsigned grid = (unsigned)cdiv(a.rows * a.kblocks, 64);
   const T* x = static_cast<const T*>(in);
   const bool fast = fast_rows<T>(in, a.ld_in, a.cols);
+  const bool wide = fast && reinterpret_cast<uintptr_t>(in) % 32 == 0 && a.ld_in * (int64_t)sizeof(T) % 32 == 0 &&
+                    a.cols % 16 == 0;
+  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(256), 0, s, a, x); };
   if (swiglu)
-    return fast ? launch_pdl(fp8_quant_rows_kernel<T, true, true>, dim3(grid), dim3(256), 0, s, a, x)
-                : launch_pdl(fp8_quant_rows_kernel<T, false, true>, dim3(grid), dim3(256), 0, s, a, x);
-  return fast ? launch_pdl(fp8_quant_rows_kernel<T, true, false>, dim3(grid), dim3(256), 0, s, a, x)
-              : launch_pdl(fp8_quant_rows_kernel<T, false, false>, dim3(grid), dim3(256), 0, s, a, x);
+    return wide ? go(fp8_quant_rows_kernel<T, 2, true>)
+                : fast ? go(fp8_quant_rows_kernel<T, 1, true>) : go(fp8_quant_rows_kernel<T, 0, true>);
+  return wide ? go(fp8_quant_rows_kernel<T, 2, false>)
+              : fast ? go(fp8_quant_rows_kernel<T, 1, false>) : go(fp8_quant_rows_kernel<T, 0, false>);
 }
 
 template <typename T, bool COLS, bool TRANS>
@@ -298,7 +393,7 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   ApiRange api_range("moe_fp8_quantize_rows");
   if (rows < 0 || cols < 1 || swiglu < 0 || swiglu > 1) return MOE_ERR_INVALID_ARG;
   const int kb = (int)cdiv(cols, kBlk);
-  if (cols > (1 << 20) || rows * kb >= (int64_t(1) << 32) - 32) return MOE_ERR_UNSUPPORTED;
+  if (cols > (1 << 20) || rows * kb >= (int64_t(1) << 31) - 64) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   const moe_status st = check_quant(type, in, ld_in, (int64_t)cols * (1 + swiglu), codes, ld_codes, cols, scales);
   if (st != MOE_OK) return st;
@@ -310,6 +405,7 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   a.ld_scales = ld_scales;
   a.cols = cols;
   a.kblocks = kb;
+  a.by_kblocks = FastDiv((uint32_t)kb);
   a.row_src = row_src;
   a.rows_used = rows_used;
   a.codes = static_cast<uint8_t*>(codes);

@@ -34,6 +34,11 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
+__device__ __forceinline__ void load32(const void* p, uint4& a, uint4& b) {  // 32-byte aligned
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
 // 16 bytes at any address, from the two aligned windows they lie in.
 __device__ __forceinline__ uint4 load16_any(const void* p) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(p);
