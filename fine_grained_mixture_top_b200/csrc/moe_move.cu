@@ -25,8 +25,8 @@ inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // ----------------------------------------------------------------- sort
-// The choices (t, k) are sorted by expert, stably, in chunks of kSortChunk.
-// Inside a chunk each warp takes 256 consecutive choices and ranks 32 at a
+// The choices (t, k) are sorted by expert, stably, in chunks of 1024 ITERS.
+// Inside a chunk each warp takes 32 ITERS consecutive choices and ranks 32 at a
 // time: lanes with the same expert find each other with match_any, and a
 // per-warp histogram in shared memory carries the count from one step to the
 // next.  The warps' histograms are then summed in order, which gives each
@@ -34,15 +34,21 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // one launch; more chunks leave their histograms in the workspace for a second
 // launch, whose blocks each add up the chunks before theirs (nchunks * E
 // values, a few KB) instead of waiting for a scan of their own.
+//
+// All of it is latency: short chunks (2 steps) where that leaves few of them,
+// long ones (8) for many choices, where every block of the second launch reads
+// all the histograms.  16384 x 8 choices over 128 experts: 11 us, with long
+// chunks 18.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortIters = 8;
-constexpr int kSortChunk = kSortThreads * kSortIters;  // ranks and kept counts fit 16 bits
-constexpr int kScatter = 2 * kSortThreads;             // choices per block of the second launch
+constexpr int kShort = 2, kLong = 8;                        // steps of a chunk
+constexpr int64_t kMostShort = 128 * kSortThreads * kShort;  // choices up to which chunks are short
+constexpr int kScatter = kSortThreads;                      // choices per block of the second launch
+inline int sort_steps(int64_t P) { return P <= kMostShort ? kShort : kLong; }
 
 struct SortArgs {
   int64_t P;  // T * K choices
-  int T, K, E, nchunks;
+  int T, K, E, nchunks, chunk;  // chunk: choices of one
   const int* topk_idx;
   const float* topk_gate;
   int* tok_ptr;
@@ -59,30 +65,39 @@ struct SortArgs {
   uint32_t* local;  // [P] rank in the chunk | kept choices before it in the chunk << 16
 };
 
-// Exclusive sum over the block's 1024 threads; *total gets the block's sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+// Over the block's 1024 threads: the exclusive sums of `v`, and the totals of v,
+// p and k, in one pass over the barriers.
+struct BlockSums {
+  int before, v, p, k;
+};
+__device__ __forceinline__ BlockSums block_sums(int v, int p, int k, int (*warp_sums)[kSortWarps]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
+    p += __shfl_xor_sync(0xffffffffu, p, o);
+    k += __shfl_xor_sync(0xffffffffu, k, o);
   }
-  __syncthreads();  // warp_sums may still be read from an earlier call
-  if (lane == 31) warp_sums[warp] = x;
+  if (lane == 31) warp_sums[0][warp] = x;
+  if (lane == 0) warp_sums[1][warp] = p, warp_sums[2][warp] = k;
   __syncthreads();
   if (warp == 0) {
-    int s = warp_sums[lane];
+    int s = warp_sums[0][lane], q = warp_sums[1][lane], r = warp_sums[2][lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += y;
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+      r += __shfl_xor_sync(0xffffffffu, r, o);
     }
-    warp_sums[lane] = s;
+    warp_sums[0][lane] = s;
+    if (lane == 0) warp_sums[1][0] = q, warp_sums[2][0] = r;
   }
   __syncthreads();
-  *total = warp_sums[kSortWarps - 1];
-  return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+  return {x - v + (warp > 0 ? warp_sums[0][warp - 1] : 0), warp_sums[0][kSortWarps - 1], warp_sums[1][0],
+          warp_sums[2][0]};
 }
 
 // The parts of a routing that no choice owns: padding rows and the tails
@@ -121,11 +136,11 @@ __device__ __forceinline__ void fill_rest(const SortArgs& a, const int* off, con
   }
 }
 
-__device__ __forceinline__ void scatter_choice(const SortArgs& a, int64_t i, int e, int row, int64_t before) {
-  const int t = (int)(i / a.K);
-  if (i == (int64_t)t * a.K) a.tok_ptr[t] = (int)before;
+// choice i < 2^31 with gate g; `before`: kept choices before it
+__device__ __forceinline__ void scatter_choice(const SortArgs& a, uint32_t i, int e, float g, int row, int64_t before) {
+  const int t = (int)(i / (uint32_t)a.K);
+  if (i == (uint32_t)t * (uint32_t)a.K) a.tok_ptr[t] = (int)before;
   if (e < 0) return;
-  const float g = __ldg(a.topk_gate + i);
   a.pair_row[before] = row;
   a.pair_expert[before] = e;
   a.pair_gate[before] = g;
@@ -135,30 +150,38 @@ __device__ __forceinline__ void scatter_choice(const SortArgs& a, int64_t i, int
 
 // Dynamic shared memory: uint16 hist[32][E] (E rounded up to even), then, in
 // the one-launch form, int off[E + 1] and cnt[E].
-template <bool ONE>
+template <bool ONE, int ITERS>
 __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs a) {
   pdl_wait();
   extern __shared__ __align__(16) uint8_t smem_sort[];
-  __shared__ int warp_sums[kSortWarps];
+  __shared__ int warp_sums[3][kSortWarps];
   __shared__ int warp_kept[kSortWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = a.E, Es = (E + 1) & ~1;
   uint16_t* hist = reinterpret_cast<uint16_t*>(smem_sort);
-  for (int i = threadIdx.x; i < Es * kSortWarps / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0u;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk + warp * (32 * kSortIters) + lane;
-  int e[kSortIters];
-  uint32_t rk[kSortIters];
+  // ONE: every block ranks all choices, and places and fills its share
+  const int64_t first = ONE ? 0 : (int64_t)blockIdx.x * (kSortThreads * ITERS);
+  const int64_t left = a.P - first;
+  const int warps = (int)min((int64_t)kSortWarps, (left + 32 * ITERS - 1) / (32 * ITERS));  // those with choices
+  for (int i = threadIdx.x; i < Es * warps / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0u;
+  const int64_t i0 = first + warp * (32 * ITERS) + lane;
+  int e[ITERS];
+  float gate[ITERS];
+  uint32_t rk[ITERS];
 #pragma unroll
-  for (int it = 0; it < kSortIters; ++it) {
+  for (int it = 0; it < ITERS; ++it) {
     const int64_t i = i0 + it * 32;
     const int v = i < a.P ? __ldg(a.topk_idx + i) : -1;
     e[it] = (unsigned)v < (unsigned)E ? v : -1;
+    gate[it] = ONE && i < a.P ? __ldg(a.topk_gate + i) : 0.f;
   }
   __syncthreads();
   uint16_t* mine = hist + warp * Es;
   uint32_t kept = 0;
 #pragma unroll
-  for (int it = 0; it < kSortIters; ++it) {
+  for (int it = 0; it < ITERS; ++it) {
+    rk[it] = 0;
+    if (i0 - lane + it * 32 >= a.P) continue;  // the whole warp
     const unsigned same = __match_any_sync(0xffffffffu, e[it]);
     const unsigned live = __ballot_sync(0xffffffffu, e[it] >= 0);
     const unsigned below = (1u << lane) - 1;
@@ -174,7 +197,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs 
   int count = 0;  // thread x < E: expert x's choices of the chunk
   if (threadIdx.x < E) {
 #pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
+    for (int w = 0; w < warps; ++w) {
       const int v = hist[w * Es + threadIdx.x];
       hist[w * Es + threadIdx.x] = (uint16_t)count;
       count += v;
@@ -186,7 +209,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs 
   if constexpr (!ONE) {
     if (threadIdx.x < E) a.hist[(size_t)blockIdx.x * E + threadIdx.x] = count;
 #pragma unroll
-    for (int it = 0; it < kSortIters; ++it) {
+    for (int it = 0; it < ITERS; ++it) {
       const int64_t i = i0 + it * 32;
       if (i >= a.P) continue;
       const uint32_t base = e[it] >= 0 ? mine[e[it]] : 0u;
@@ -195,67 +218,80 @@ __global__ void __launch_bounds__(kSortThreads) sort_rank_kernel(const SortArgs 
   } else {
     int* off = reinterpret_cast<int*>(smem_sort + (size_t)Es * kSortWarps * 2);
     int* cnt = off + E + 1;
-    int rows, pairs;
-    const int o = block_scan((count + kTile - 1) / kTile * kTile, warp_sums, &rows);
-    block_scan(count, warp_sums, &pairs);
+    const BlockSums sum = block_sums((count + kTile - 1) / kTile * kTile, count, 0, warp_sums);
     if (threadIdx.x < E) {
-      off[threadIdx.x] = o;
+      off[threadIdx.x] = sum.before;
       cnt[threadIdx.x] = count;
     }
-    if (threadIdx.x == 0) off[E] = rows;
+    if (threadIdx.x == 0) off[E] = sum.v;
     __syncthreads();
 #pragma unroll
-    for (int it = 0; it < kSortIters; ++it) {
+    for (int it = 0; it < ITERS; ++it) {
       const int64_t i = i0 + it * 32;
-      if (i >= a.P) continue;
+      if (i >= a.P || warp % gridDim.x != blockIdx.x) continue;
       const int x = e[it];
       const int row = x >= 0 ? off[x] + mine[x] + (int)(rk[it] & 0xffffu) : -1;
-      scatter_choice(a, i, x, row, (int64_t)kept0 + (rk[it] >> 16));
+      scatter_choice(a, (uint32_t)i, x, gate[it], row, (int64_t)kept0 + (rk[it] >> 16));
     }
-    fill_rest(a, off, cnt, pairs);
+    fill_rest(a, off, cnt, sum.p);
   }
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortArgs a) {
   pdl_wait();
   extern __shared__ __align__(16) uint8_t smem_sort[];
-  __shared__ int warp_sums[kSortWarps];
+  __shared__ int warp_sums[3][kSortWarps];
   const int E = a.E;
   int* off = reinterpret_cast<int*>(smem_sort);  // [E + 1]
   int* cnt = off + E + 1;                        // [E]
   int* base = cnt + E;                           // [E] first row of this chunk's choices of the expert
-  const int chunk = (int)((int64_t)blockIdx.x * kScatter / kSortChunk);
+  const int64_t i = (int64_t)blockIdx.x * kScatter + threadIdx.x;  // this thread's choice
+  const bool live = i < a.P;
+  const int v = live ? __ldg(a.topk_idx + i) : -1;
+  const float gate = live ? __ldg(a.topk_gate + i) : 0.f;
+  const uint32_t local = live ? __ldg(a.local + i) : 0u;
+  const int chunk = (int)((int64_t)blockIdx.x * kScatter / a.chunk);
+  // column sums of the histograms, before this chunk and in all: several threads
+  // per expert where there are few experts, so that the loads are in flight together
+  int cols = 32;
+  while (cols < E) cols <<= 1;
+  const int parts = kSortThreads / cols, part = threadIdx.x / cols, col = threadIdx.x & (cols - 1);
   int before = 0, count = 0;
-  if (threadIdx.x < E) {
-    const int* h = a.hist + threadIdx.x;
-#pragma unroll 8
-    for (int c = 0; c < a.nchunks; ++c) {
+  if (col < E) {
+    const int* h = a.hist + col;
+#pragma unroll 16
+    for (int c = part; c < a.nchunks; c += parts) {
       const int v = __ldg(h + (size_t)c * E);
       before += c < chunk ? v : 0;
       count += v;
     }
   }
-  int rows, pairs, kept0;
-  const int o = block_scan((count + kTile - 1) / kTile * kTile, warp_sums, &rows);
-  block_scan(count, warp_sums, &pairs);
-  block_scan(before, warp_sums, &kept0);
-  if (threadIdx.x < E) {
-    off[threadIdx.x] = o;
-    cnt[threadIdx.x] = count;
-    base[threadIdx.x] = o + before;
-  }
-  if (threadIdx.x == 0) off[E] = rows;
+  int* sum = base;  // [2][1024], then base
+  sum[threadIdx.x] = before;
+  sum[kSortThreads + threadIdx.x] = count;
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kScatter / kSortThreads; ++j) {
-    const int64_t i = (int64_t)blockIdx.x * kScatter + j * kSortThreads + threadIdx.x;
-    if (i >= a.P) continue;
-    const int v = __ldg(a.topk_idx + i);
-    const int e = (unsigned)v < (unsigned)E ? v : -1;
-    const uint32_t l = __ldg(a.local + i);
-    scatter_choice(a, i, e, e >= 0 ? base[e] + (int)(l & 0xffffu) : -1, (int64_t)kept0 + (l >> 16));
+  if (threadIdx.x < cols) {
+    for (int p = 1; p < parts; ++p) {
+      before += sum[p * cols + threadIdx.x];
+      count += sum[kSortThreads + p * cols + threadIdx.x];
+    }
+  } else {
+    before = count = 0;
   }
-  fill_rest(a, off, cnt, pairs);
+  const BlockSums all = block_sums((count + kTile - 1) / kTile * kTile, count, before, warp_sums);
+  if (threadIdx.x < E) {
+    off[threadIdx.x] = all.before;
+    cnt[threadIdx.x] = count;
+    base[threadIdx.x] = all.before + before;
+  }
+  if (threadIdx.x == 0) off[E] = all.v;
+  __syncthreads();
+  if (live) {
+    const int e = (unsigned)v < (unsigned)E ? v : -1;
+    scatter_choice(a, (uint32_t)i, e, gate, e >= 0 ? base[e] + (int)(local & 0xffffu) : -1,
+                   (int64_t)all.k + (local >> 16));
+  }
+  fill_rest(a, off, cnt, all.p);
 }
 
 cudaError_t launch_sort(SortArgs a, cudaStream_t s) {
@@ -263,17 +299,19 @@ cudaError_t launch_sort(SortArgs a, cudaStream_t s) {
   const size_t hist = (size_t)Es * kSortWarps * 2, seg = (size_t)(2 * a.E + 1) * 4;
   // limits set for the largest E, so that they are set once
   constexpr int kMost = 1024 * kSortWarps * 2 + 2049 * 4;
-  if (a.nchunks <= 1) {
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(sort_rank_kernel<true>), kMost);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(sort_rank_kernel<true>, dim3(1), dim3(kSortThreads), hist + seg, s, a);
-  }
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(sort_rank_kernel<false>), kMost);
+  const bool brief = a.chunk == kSortThreads * kShort;
+  auto rank = a.nchunks <= 1 ? sort_rank_kernel<true, kShort>
+                             : brief ? sort_rank_kernel<false, kShort> : sort_rank_kernel<false, kLong>;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(rank), kMost);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(sort_rank_kernel<false>, dim3((unsigned)a.nchunks), dim3(kSortThreads), hist, s, a);
+  // as many blocks as the rows to fill need (one alone took 10.4 us for 64 x 8
+  // choices over 256 experts, 33280 rows, 5.5 with the work spread)
+  const int64_t fill = std::max<int64_t>(1, std::min<int64_t>(32, cdiv(a.R_max, 2 * kSortThreads)));
+  if (a.nchunks <= 1) return launch_pdl(rank, dim3((unsigned)fill), dim3(kSortThreads), hist + seg, s, a);
+  e = launch_pdl(rank, dim3((unsigned)a.nchunks), dim3(kSortThreads), hist, s, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(sort_scatter_kernel, dim3((unsigned)cdiv(a.P, kScatter)), dim3(kSortThreads),
-                    (size_t)(3 * a.E + 1) * 4, s, a);
+  return launch_pdl(sort_scatter_kernel, dim3((unsigned)std::max(fill, cdiv(a.P, kScatter))), dim3(kSortThreads),
+                    (size_t)(2 * a.E + 1 + 2 * kSortThreads) * 4, s, a);
 }
 
 // ----------------------------------------------------------------- rows
@@ -670,7 +708,7 @@ moe_status sort_plan(int64_t T, int32_t E, int32_t K, int64_t* P, int64_t* R, si
   if (E > 1024 || K > 32 || T * (int64_t)K >= (int64_t(1) << 31) - 4096 * 1024) return MOE_ERR_UNSUPPORTED;
   *P = T * K;
   *R = cdiv(*P + (int64_t)(kTile - 1) * std::min<int64_t>(E, *P), kTile) * kTile;
-  const int64_t chunks = cdiv(*P, kSortChunk);
+  const int64_t chunks = cdiv(*P, kSortThreads * sort_steps(*P));
   *ws = chunks <= 1 ? 0 : align256((size_t)chunks * E * sizeof(int)) + align256((size_t)*P * sizeof(uint32_t));
   return MOE_OK;
 }
@@ -717,7 +755,8 @@ moe_status moe_sort_pairs(int64_t T, int32_t E, int32_t K, const moe_routing* rt
   a.T = (int)T;
   a.K = K;
   a.E = E;
-  a.nchunks = (int)cdiv(P, kSortChunk);
+  a.chunk = kSortThreads * sort_steps(P);
+  a.nchunks = (int)cdiv(P, a.chunk);
   a.topk_idx = rt->topk_idx;
   a.topk_gate = rt->topk_gate;
   a.tok_ptr = rt->tok_ptr;

@@ -71,6 +71,7 @@ SORTS = [  # T, E, K, drop, distinct
     (300, 1024, 32, 0.1, True), (256, 8, 32, 0.0, False),       # one chunk exactly full, experts chosen twice
     (8193, 17, 1, 0.0, False), (5000, 128, 8, 0.2, True), (4096, 1023, 5, 0.3, False), (20000, 2, 2, 0.0, True),
     (600, 40, 4, 1.0, True), (16385, 1, 1, 0.5, False),
+    (2048, 9, 1, 0.1, False), (2049, 1024, 1, 0.0, False), (131072, 600, 2, 0.05, False), (87382, 33, 3, 0.2, False),
 ]
 
 
