@@ -93,21 +93,32 @@ __device__ __forceinline__ void tc_wait_ld_pair(uint32_t (&a)[32], uint32_t (&b)
                : "memory");
 }
 
-// acc += 32 columns of a block's sums times the scales.  (Packed two-value FMAs
-// issue half as many instructions, but need their operands in register pairs:
-// the moves into them cost more than they save, 355 against 335 us for 65536
-// rows x 2048 x 2048 over 16 experts.)
+// acc += 32 columns of a block's sums times the scales.  BROWS, with its product
+// per value besides the FMA, computes two values per instruction (weight gradient
+// of 131072 rows over 128 experts, 1536 x 512: 180 us, one at a time 186); for the
+// FMA alone the moves into register pairs cost more than that saves (65536 rows x
+// 2048 x 2048 over 16 experts: 335 us one at a time, 355 in pairs).
+__device__ __forceinline__ uint64_t pack2f(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 template <bool BROWS>
 __device__ __forceinline__ void add_columns(float* acc, const uint32_t (&v)[32], float s, const float* cols) {
+  if constexpr (!BROWS) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float f[4] = {s, s, s, s};
-    if constexpr (BROWS) {
-      const float4 w = reinterpret_cast<const float4*>(cols)[j];
-      f[0] *= w.x, f[1] *= w.y, f[2] *= w.z, f[3] *= w.w;
+    for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(v[j]), s, acc[j]);
+  } else {
+    const uint64_t s2 = pack2f(s, s);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint64_t w = reinterpret_cast<const uint64_t*>(cols)[j];
+      const uint64_t x = pack2f(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+      uint64_t f, a = pack2f(acc[2 * j], acc[2 * j + 1]);
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(f) : "l"(w), "l"(s2));
+      asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(x), "l"(f));
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[2 * j]), "=f"(acc[2 * j + 1]) : "l"(a));
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) acc[4 * j + u] = fmaf(__uint_as_float(v[4 * j + u]), f[u], acc[4 * j + u]);
   }
 }
 // One block's sums: acc += TMEM slot (128 columns of this thread's row) times
@@ -563,12 +574,12 @@ __global__ void __maxnreg__((Fp8SmallShape::kMaxReg)) fp8_gemm_small_kernel(cons
 // holds its 128 rows of the result: 128 columns in each of two epilogue
 // warpgroups' registers.  TMEM holds two 256-column slots.
 //
-// What paces it: a block is four MMAs of 128 clocks, its operands take 385 ns
-// from L2 at the 85 GB/s that an SM fills its shared memory with, and its
-// epilogue is one FMA per value (256 clocks; BROWS adds a product) behind two
-// rounds of TMEM loads.  Measured per block and CTA: 385 ns for the loads and
-// barriers alone, 615 ns with everything in short runs, 760 ns in long ones, where
-// the power cap lowers the clock.
+// What paces it, per block and CTA in short runs: 615 ns with everything; about
+// 450 without the epilogue's arithmetic and the MMAs (the operands come from L2 at
+// the 85 GB/s that an SM fills its shared memory with), 470 without the operand
+// loads and that arithmetic (the MMAs, 512 clocks at the tensor core's peak), 510
+// without the MMAs.  The three overlap through four operand stages and two slots.
+// In long runs the power cap lowers the clock, and a block takes 735 ns.
 //
 // GROUPED: a tile is two consecutive 128-row tiles of one expert; where an
 // expert's last tile is alone, the second CTA loads no A, lets its accumulator

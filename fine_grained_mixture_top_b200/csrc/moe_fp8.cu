@@ -123,7 +123,8 @@ struct QuantArgs {
   int64_t rows, ld_in, ld_codes, ld_scales;
   int cols, kblocks;           // blocks of a row (rows kernel)
   FastDiv by_kblocks;
-  const int* row_src;          // nullable: the input row of each row, -1: zeros
+  const int* row_src;          // nullable: the input row of each row; outside [0, in_rows): zeros
+  int64_t in_rows;
   const int* rows_used;        // nullable: rows from here on are left as they are
   uint8_t* codes;
   float* scales;
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const QuantArgs a, 
   const int kb = (int)(unit - row * (uint32_t)a.kblocks);
   const int64_t used = a.rows_used ? min((int64_t)__ldg(a.rows_used), a.rows) : a.rows;
   const bool live = row < used;
-  const int64_t from = live ? (a.row_src ? (int64_t)__ldg(a.row_src + row) : (int64_t)row) : -1;
+  int64_t from = live ? (a.row_src ? (int64_t)__ldg(a.row_src + row) : (int64_t)row) : -1;
+  if (a.row_src && from >= a.in_rows) from = -1;
   const int e0 = kb * kBlk + 16 * l;
   const int width = from < 0 ? 0 : a.cols;  // nothing to load: zeros
   const T* src = in + (from < 0 ? 0 : from) * a.ld_in;
@@ -238,8 +240,15 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const QuantArgs a, 
 // packs 4 codes of a column into a word for the transposed store.
 //   COLS   one scale per column of the tile, codes transposed [cols, rows]
 //   !COLS  one scale per tile; TRANS: codes transposed
-template <typename T, bool FAST, bool COLS, bool TRANS>
-__global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const QuantArgs a, const T* __restrict__ in0) {
+//   GATHER the tile's rows are in[row_src[r]]
+// Thread blocks per SM that the registers are cut for (a tile is loads, a
+// barrier, stores, so that several have to overlap), as measured: 16-bit columns
+// 4 (32768 x 2048: 51 us, at 2 69), blocks 5 or, unaligned, 6 (32 x 1001 x 1003:
+// 32 us, at 4 36); fp32 3.
+template <typename T, bool FAST, bool COLS>
+constexpr int kTileBlocks = sizeof(T) == 4 ? 3 : COLS ? 4 : FAST ? 5 : 6;
+template <typename T, bool FAST, bool COLS, bool TRANS, bool GATHER>
+__global__ void __launch_bounds__(256, kTileBlocks<T, FAST, COLS>) fp8_quant_tile_kernel(const QuantArgs a, const T* __restrict__ in0) {
   pdl_wait();
   __shared__ uint32_t words[TRANS ? kBlk * 33 : 1];  // [column][4-row group], one word of padding
   __shared__ float part[8][COLS ? kBlk : 1];
@@ -255,13 +264,20 @@ __global__ void __launch_bounds__(256) fp8_quant_tile_kernel(const QuantArgs a, 
   const int col = 8 * (lane & 15);
   const int group = 2 * warp + (lane >> 4);  // rows 4 group .. + 3, and 64 more
   Raw8<T> x[8];
+  int from[8];  // row of the tile (GATHER: of `in`), -1: zeros
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + 4 * group + (i & 3) + 64 * (i >> 2);
-    int64_t from = r < rows ? r : -1;
-    if (from >= 0 && a.row_src) from = __ldg(a.row_src + r);
-    if (from >= 0) x[i] = load8<T, FAST>(in + from * a.ld_in, c0 + col, a.cols);
-    else x[i].clear();
+    const int r = 4 * group + (i & 3) + 64 * (i >> 2);
+    from[i] = r0 + r < rows ? r : -1;
+    if (GATHER && from[i] >= 0) from[i] = __ldg(a.row_src + r0 + r);
+  }
+  const T* first = GATHER ? in : in + r0 * a.ld_in;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (from[i] >= 0 && (!GATHER || from[i] < a.in_rows))
+      x[i] = load8<T, FAST>(first + from[i] * a.ld_in, c0 + col, a.cols);
+    else
+      x[i].clear();
   }
   float f[8];
   if constexpr (COLS) {
@@ -352,8 +368,14 @@ cudaError_t launch_tiles(const QuantArgs& a, int E, const void* in, cudaStream_t
   const dim3 grid((unsigned)cdiv(a.cols, kBlk), (unsigned)cdiv(a.rows, kBlk), (unsigned)E);
   const T* x = static_cast<const T*>(in);
   const bool fast = fast_rows<T>(in, a.ld_in, a.cols) && a.plane_in * (int64_t)sizeof(T) % 16 == 0;
-  return fast ? launch_pdl(fp8_quant_tile_kernel<T, true, COLS, TRANS>, grid, dim3(256), 0, s, a, x)
-              : launch_pdl(fp8_quant_tile_kernel<T, false, COLS, TRANS>, grid, dim3(256), 0, s, a, x);
+  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(256), 0, s, a, x); };
+  if constexpr (COLS) {
+    if (a.row_src)
+      return fast ? go(fp8_quant_tile_kernel<T, true, COLS, TRANS, true>)
+                  : go(fp8_quant_tile_kernel<T, false, COLS, TRANS, true>);
+  }
+  return fast ? go(fp8_quant_tile_kernel<T, true, COLS, TRANS, false>)
+              : go(fp8_quant_tile_kernel<T, false, COLS, TRANS, false>);
 }
 
 int64_t elem_size(moe_dtype t) { return t == MOE_F32 ? 4 : (t == MOE_BF16 || t == MOE_F16) ? 2 : 0; }
@@ -387,11 +409,11 @@ using namespace moe;
 
 extern "C" {
 
-moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
-                                 const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
+moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
                                  int64_t ld_codes, float* scales, int64_t ld_scales, void* stream) {
   ApiRange api_range("moe_fp8_quantize_rows");
-  if (rows < 0 || cols < 1 || swiglu < 0 || swiglu > 1) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || in_rows < 0 || cols < 1 || swiglu < 0 || swiglu > 1) return MOE_ERR_INVALID_ARG;
   const int kb = (int)cdiv(cols, kBlk);
   if (cols > (1 << 20) || rows * kb >= (int64_t(1) << 31) - 64) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
@@ -407,6 +429,7 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   a.kblocks = kb;
   a.by_kblocks = FastDiv((uint32_t)kb);
   a.row_src = row_src;
+  a.in_rows = in_rows;
   a.rows_used = rows_used;
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;
@@ -416,11 +439,11 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   return MOE_OK;
 }
 
-moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
-                                 const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
+moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
                                  float* scales, int64_t ld_scales, void* stream) {
   ApiRange api_range("moe_fp8_quantize_cols");
-  if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || in_rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
   if (cols > (1 << 20) || cdiv(rows, kBlk) > 65535) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   const moe_status st = check_quant(type, in, ld_in, cols, codes, ld_codes, rows, scales);
@@ -433,6 +456,7 @@ moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, 
   a.ld_scales = ld_scales;
   a.cols = cols;
   a.row_src = row_src;
+  a.in_rows = in_rows;
   a.rows_used = rows_used;
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;

@@ -103,10 +103,10 @@ def lib() -> ctypes.CDLL:
         L.moe_unpermute.argtypes = L.moe_permute.argtypes
         L.moe_unpermute_bwd.argtypes = [c_int64, c_int32, c_int32, P(MoeRouting), c_int32, c_int64, c_void_p, c_int64,
                                         c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p]
-        L.moe_fp8_quantize_rows.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_void_p, c_int32,
-                                            c_void_p, c_int64, c_void_p, c_int64, c_void_p]
-        L.moe_fp8_quantize_cols.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_void_p, c_void_p,
-                                            c_int64, c_void_p, c_int64, c_void_p]
+        L.moe_fp8_quantize_rows.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int64, c_int32, c_void_p,
+                                            c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
+        L.moe_fp8_quantize_cols.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int64, c_int32, c_void_p,
+                                            c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
         L.moe_fp8_quantize_blocks.argtypes = [c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
                                               c_void_p, c_void_p]
         L.moe_fp8_gemm.argtypes = [c_int64, c_int64, c_int64, c_int32, P(MoeRouting), c_void_p, c_int64, c_void_p,
@@ -326,25 +326,33 @@ def mx_quantize_cols(w, stream=None):
 # Rows sorted by expert and back.  These check their tensors, allocate what the
 # caller leaves out, and run on the tensors' device.
 
-_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2, "torch.float8_e4m3fn": 3}
+_torch = None
+_DTYPES = {}
+
+
+def _th():
+    """torch, imported on first use (an import statement in every one of these
+    short calls adds up)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3})
+        _torch = torch
+    return _torch
 
 
 def _dtype_code(t, what: str, most: int = 2) -> int:
-    code = _DTYPES.get(str(t.dtype), 99)
+    code = _DTYPES.get(t.dtype, 99)
     if code > most:
         raise TypeError(f"{what}: {t.dtype} is not supported")
     return code
 
 
-def _want(cond: bool, message: str):
-    if not cond:
-        raise ValueError(message)
-
-
-def _width(t, name: str) -> int:
-    if t.dim() != 2:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
-    return t.shape[1]
+def _shape2(t, name: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected two dimensions")
+    return shape
 
 
 def _matrix(t, name: str, rows: int, cols: int, device, dtype=None) -> int:
@@ -371,22 +379,19 @@ def _matrix(t, name: str, rows: int, cols: int, device, dtype=None) -> int:
 
 def _away(device) -> bool:
     """Is `device` another than the current one?  (It then has to be made current for the call.)"""
-    import torch
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}: a CUDA device is needed")
-    return torch._C._cuda_getDevice() != device.index
+    return _torch._C._cuda_getDevice() != device.index
 
 
 def _stream_on(stream, device) -> int:
     """Handle of `stream`, or of the current stream of the (current) device
     (without the Python object around it: 0.1 instead of 3.4 us)."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return _torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _on(device, fn, *args, **kw):
-    import torch
-    with torch.cuda.device(device):
+    with _torch.cuda.device(device):
         return fn(*args, **kw)
 
 
@@ -396,10 +401,9 @@ def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=N
     Routing of an earlier call with the same T, K and E can be given again as
     `routing`; it is overwritten.  ws: a uint8 workspace of moe_sort_sizes'
     bytes (default: allocated)."""
-    import torch
+    torch = _th()
     dev = topk_idx.device
-    K = _width(topk_idx, "topk_idx")
-    T = topk_idx.shape[0]
+    T, K = _shape2(topk_idx, "topk_idx")
     for t, name, dt in ((topk_idx, "topk_idx", torch.int32), (topk_gate, "topk_gate", torch.float32)):
         if _matrix(t, name, T, K, dev, dt) != K:
             raise ValueError(f"{name}: must be contiguous")
@@ -423,6 +427,8 @@ def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=N
     elif ws.dtype != torch.uint8 or ws.device != dev:
         raise ValueError(f"ws: uint8 on {dev} expected")
     r, st = routing.tensors, routing.struct
+    if r.get("logits") is not None or r.get("probs") is not None:
+        raise ValueError("routing: not one that sort_pairs made")
     if r["tok_ptr"].shape[0] != T + 1 or r["counts"].shape[0] != E or r["tok_ptr"].device != dev:
         raise ValueError("routing: made for another T, E or device")
     r["topk_idx"], r["topk_gate"] = topk_idx, topk_gate
@@ -443,31 +449,38 @@ def permute(routing: Routing, src, rows=None, stream=None):
     """rows [R_max, width]: src [T, width] in expert order, zeros in the padding
     rows.  Rows past the last expert's segment are left as they were (in a
     tensor allocated here: undefined)."""
+    _th()
     T, E, R, dev = _routed(routing)
     code = _dtype_code(src, "src", 3)
-    width = _width(src, "src")
+    width = _shape2(src, "src")[1]
     ld = _matrix(src, "src", T, width, dev)
     if _away(dev):
         return _on(dev, permute, routing, src, rows, stream)
+    ldr = width
     if rows is None:
         rows = src.new_empty((R, width))
-    ldr = _matrix(rows, "rows", R, width, dev, src.dtype)
+    else:
+        ldr = _matrix(rows, "rows", R, width, dev, src.dtype)
     _check(lib().moe_permute(T, E, ctypes.byref(routing.struct), code, width, _ptr(src), ld, _ptr(rows), ldr,
                              _stream_on(stream, dev)), "moe_permute")
     return rows
 
 
 def _sum_rows(fn, what, routing, rows, out, stream):
+    _th()
     T, E, R, dev = _routed(routing)
     code = _dtype_code(rows, "rows")
-    width = _width(rows, "rows")
+    width = _shape2(rows, "rows")[1]
     ld = _matrix(rows, "rows", R, width, dev)
     if _away(dev):
         return _on(dev, _sum_rows, fn, what, routing, rows, out, stream)
+    ldo = width
     if out is None:
         out = rows.new_empty((T, width))
-    ldo = _matrix(out, "out", T, width, dev, rows.dtype)
-    _check(fn(T, E, ctypes.byref(routing.struct), code, width, _ptr(rows), ld, _ptr(out), ldo, _stream_on(stream, dev)), what)
+    else:
+        ldo = _matrix(out, "out", T, width, dev, rows.dtype)
+    _check(fn(T, E, ctypes.byref(routing.struct), code, width, _ptr(rows), ld, _ptr(out), ldo,
+              _stream_on(stream, dev)), what)
     return out
 
 
@@ -486,18 +499,20 @@ def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: b
     in the places of topk_idx, 0 for dropped choices; with pairs=True it is
     [P_max] in pair order (for moe_token_round's routings), where entries past
     the pairs in use are left as they were."""
-    import torch
+    torch = _th()
     T, E, R, dev = _routed(routing)
     code = _dtype_code(rows, "rows")
-    width = _width(rows, "rows")
+    width = _shape2(rows, "rows")[1]
     ld = _matrix(rows, "rows", R, width, dev)
     ldo = _matrix(dout, "dout", T, width, dev, rows.dtype)
     K = routing.tensors["topk_idx"].shape[1]
     if _away(dev):
         return _on(dev, unpermute_bwd, routing, dout, rows, drows, dgate, pairs, stream)
+    ldd = width
     if drows is None:
         drows = rows.new_empty((R, width))
-    ldd = _matrix(drows, "drows", R, width, dev, rows.dtype)
+    else:
+        ldd = _matrix(drows, "drows", R, width, dev, rows.dtype)
     shape = (routing.struct.P_max,) if pairs else (T, K)
     if dgate is None:
         dgate = torch.empty(shape, dtype=torch.float32, device=dev)
@@ -518,15 +533,14 @@ def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: b
 
 
 def _new_codes(lead, cols: int, device):
-    import torch
+    torch = _th()
     ld = (cols + 15) // 16 * 16
-    codes = torch.empty(*lead, ld, dtype=torch.float8_e4m3fn, device=device)
+    codes = torch.empty((*lead, ld), dtype=torch.float8_e4m3fn, device=device)
     return codes if ld == cols else codes[..., :cols]
 
 
 def _codes(t, name: str, rows: int, cols: int, device) -> int:
-    import torch
-    ld = _matrix(t, name, rows, cols, device, torch.float8_e4m3fn)
+    ld = _matrix(t, name, rows, cols, device, _torch.float8_e4m3fn)
     if rows <= 1:
         ld = (cols + 15) // 16 * 16
     if ld % 16 or t.data_ptr() % 16:
@@ -535,10 +549,9 @@ def _codes(t, name: str, rows: int, cols: int, device) -> int:
 
 
 def _i32(t, name: str, n: int, device):
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.int32:
+    if t.dtype != _torch.int32:
         raise TypeError(f"{name}: {t.dtype}, expected torch.int32")
     if t.device != device or t.dim() != 1 or t.shape[0] < n or (t.shape[0] > 1 and t.stride(0) != 1):
         raise ValueError(f"{name}: {n} contiguous values on {device} expected")
@@ -546,11 +559,10 @@ def _i32(t, name: str, n: int, device):
 
 
 def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
-    import torch
+    torch = _th()
     code = _dtype_code(x, "x")
-    width = _width(x, "x")
+    n_in, width = _shape2(x, "x")
     dev = x.device
-    n_in = x.shape[0]
     ld = _matrix(x, "x", n_in, width, dev)
     if swiglu and width % 2:
         raise ValueError(f"x: {width} columns, expected gate and up halves")
@@ -561,26 +573,30 @@ def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
     if _away(dev):
         return _on(dev, _quantize, cols_form, x, row_src, rows_used, swiglu, codes, scales, stream)
     out, blocks = ((cols, rows), -(-rows // 128)) if cols_form else ((rows, cols), -(-cols // 128))
+    ldc, lds = (out[1] + 15) // 16 * 16, out[0]
     if codes is None:
         codes = _new_codes(out[:1], out[1], dev)
-    if scales is None:
-        scales = torch.empty(blocks, out[0], dtype=torch.float32, device=dev)
-    ldc = _codes(codes, "codes", *out, dev)
-    lds = _matrix(scales, "scales", blocks, out[0], dev, torch.float32)
-    if cols_form:
-        _check(lib().moe_fp8_quantize_cols(code, _ptr(x), ld, rows, cols, src, used, _ptr(codes), ldc, _ptr(scales),
-                                           lds, _stream_on(stream, dev)), "moe_fp8_quantize_cols")
     else:
-        _check(lib().moe_fp8_quantize_rows(code, _ptr(x), ld, rows, cols, src, used, 1 if swiglu else 0, _ptr(codes),
-                                           ldc, _ptr(scales), lds, _stream_on(stream, dev)), "moe_fp8_quantize_rows")
+        ldc = _codes(codes, "codes", *out, dev)
+    if scales is None:
+        scales = torch.empty((blocks, lds), dtype=torch.float32, device=dev)
+    else:
+        lds = _matrix(scales, "scales", blocks, lds, dev, torch.float32)
+    if cols_form:
+        _check(lib().moe_fp8_quantize_cols(code, _ptr(x), ld, n_in, rows, cols, src, used, _ptr(codes), ldc,
+                                           _ptr(scales), lds, _stream_on(stream, dev)), "moe_fp8_quantize_cols")
+    else:
+        _check(lib().moe_fp8_quantize_rows(code, _ptr(x), ld, n_in, rows, cols, src, used, 1 if swiglu else 0,
+                                           _ptr(codes), ldc, _ptr(scales), lds, _stream_on(stream, dev)),
+               "moe_fp8_quantize_rows")
     return codes, scales
 
 
 def fp8_quantize_rows(x, row_src=None, rows_used=None, swiglu: bool = False, codes=None, scales=None, stream=None):
     """x [rows, cols] -> (codes [rows, cols], scales [ceil(cols / 128), rows]).
-    row_src [R] int32: row r of the result holds x[row_src[r]], zeros where it
-    is -1; its entries must be rows of x.  rows_used: a device int32; rows from
-    there on are left as they were.  swiglu: x is [rows, 2 cols] and
+    row_src [R] int32: row r of the result holds x[row_src[r]], zeros where that
+    is no row of x (-1).  rows_used: a device int32; rows from there on are left
+    as they were.  swiglu: x is [rows, 2 cols] and
     silu(x[:, :cols]) * x[:, cols:] is quantized."""
     return _quantize(False, x, row_src, rows_used, swiglu, codes, scales, stream)
 
@@ -596,7 +612,7 @@ def fp8_quantize_blocks(w, transpose: bool, codes=None, scales=None, stream=None
     """w [E, K, N] or [K, N] (contiguous) -> codes and one scale per 128 x 128
     block: [.., K, N] and [.., ceil(K/128), ceil(N/128)], or with transpose
     [.., N, K] and [.., ceil(N/128), ceil(K/128)]."""
-    import torch
+    torch = _th()
     code = _dtype_code(w, "w")
     if w.dim() not in (2, 3) or not w.is_contiguous():
         raise ValueError(f"w: a contiguous [E, K, N] or [K, N] expected, got {tuple(w.shape)}")
@@ -638,10 +654,10 @@ def _planes(t, name: str, shape, device) -> int:
 
 def _out(out, name, shape, device):
     """bf16 result [.., rows, cols], its rows 16-byte aligned; returns (tensor, row stride)."""
-    import torch
+    torch = _torch
     if out is None:
         ld = (shape[-1] + 7) // 8 * 8
-        out = torch.empty(*shape[:-1], ld, dtype=torch.bfloat16, device=device)
+        out = torch.empty((*shape[:-1], ld), dtype=torch.bfloat16, device=device)
         return out if ld == shape[-1] else out[..., :shape[-1]], ld
     if out.shape != shape:
         raise ValueError(f"{name}: shape {tuple(out.shape)}, expected {tuple(shape)}")
@@ -661,10 +677,9 @@ def fp8_gemm(a, sa, b, sb, routing: Routing | None = None, out=None, stream=None
     scales sa [ceil(K/128), M] and sb [ceil(N/128), ceil(K/128)].  With a
     routing: a [R_max, K] in expert order, b [E, N, K], sb [E, .., ..]; rows
     past the last segment are left as they were (undefined in a new tensor)."""
-    import torch
+    torch = _th()
     dev = a.device
-    K = _width(a, "a")
-    M = a.shape[0]
+    M, K = _shape2(a, "a")
     lda = _codes(a, "a", M, K, dev)
     if routing is None:
         E, lead = 1, ()
@@ -687,7 +702,8 @@ def fp8_gemm(a, sa, b, sb, routing: Routing | None = None, out=None, stream=None
         return _on(dev, fp8_gemm, a, sa, b, sb, routing, out, stream)
     out, ldo = _out(out, "out", (M, N), dev)
     _check(lib().moe_fp8_gemm(M, N, K, E, None if routing is None else ctypes.byref(routing.struct), _ptr(a), lda,
-                              _ptr(sa), lds, _ptr(b), ldb, _ptr(sb), _ptr(out), ldo, _stream_on(stream, dev)), "moe_fp8_gemm")
+                              _ptr(sa), lds, _ptr(b), ldb, _ptr(sb), _ptr(out), ldo, _stream_on(stream, dev)),
+           "moe_fp8_gemm")
     return out
 
 
@@ -696,11 +712,10 @@ def fp8_gemm_dw(a, sa, b, sb, routing: Routing | None = None, out=None, stream=N
     transposed, both as fp8_quantize_cols leaves them (sa [ceil(tokens/128), M],
     sb [.., N]).  With a routing the tokens are its rows and out is [E, M, N],
     each expert's product over its own rows."""
-    import torch
+    torch = _th()
     dev = a.device
-    K = _width(a, "a")
-    _width(b, "b")
-    M, N = a.shape[0], b.shape[0]
+    M, K = _shape2(a, "a")
+    N = _shape2(b, "b")[0]
     lda, ldb = _codes(a, "a", M, K, dev), _codes(b, "b", N, K, dev)
     kb = (K + 127) // 128
     ldsa = _matrix(sa, "sa", kb, M, dev, torch.float32)

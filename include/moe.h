@@ -392,8 +392,9 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
  * moe_fp8_quantize_rows: in[rows, cols] (rows ld_in elements apart) -> codes
  *   [rows, ld_codes], scales[ceil(cols / 128), ld_scales] (ld_scales >= rows):
  *   one per row and 128 columns.  row_src (nullable, [rows]): row r holds
- *   in[row_src[r]], zeros where it is -1 (a routing's row_tok gathers the
- *   tokens into expert order).  rows_used (nullable, one device int): rows from
+ *   in[row_src[r]], zeros where that is outside [0, in_rows), as -1 is (a
+ *   routing's row_tok gathers the tokens into expert order); in_rows is not
+ *   looked at without row_src.  rows_used (nullable, one device int): rows from
  *   *rows_used on are left as they were (a routing's offsets + E).  swiglu = 1:
  *   in[.., 2 cols], and silu(in[c]) * in[cols + c] is quantized.
  * moe_fp8_quantize_cols: the same input -> codes[cols, ld_codes] transposed
@@ -404,11 +405,11 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
  *   scales[E, ceil(K/128), ceil(N/128)]; 1: codes[E, N, ld_codes],
  *   scales[E, ceil(N/128), ceil(K/128)].
  */
-moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
-                                 const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
+moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
                                  int64_t ld_codes, float* scales, int64_t ld_scales, void* stream);
-moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t rows, int32_t cols,
-                                 const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
+moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
                                  float* scales, int64_t ld_scales, void* stream);
 moe_status moe_fp8_quantize_blocks(moe_dtype type, const void* in, int32_t E, int32_t K, int32_t N, int32_t transpose,
                                    void* codes, int64_t ld_codes, float* scales, void* stream);
@@ -427,8 +428,10 @@ moe_status moe_fp8_quantize_blocks(moe_dtype type, const void* in, int32_t E, in
  * moe_fp8_gemm_dw: the weight gradient, both operands with a scale per row and
  *   block of 128 tokens (moe_fp8_quantize_cols): C[m, n] = sum over blocks of
  *   sA[b, m] sB[b, n] (A_b[m] . B_b[n]).  rt NULL: one product over K tokens,
- *   C[M, ldc]; rt set: C[E, M, ldc], C[e] summed over expert e's rows, zeros
- *   for an expert without rows; K = the rows' capacity (a multiple of 128).
+ *   C[M, ldc]; rt set: C[E, M, ldc], C[e] summed over all rows of expert e's
+ *   segment (padding rows must hold codes of 0, as the quantizer leaves rows of
+ *   zeros), zeros for an expert without rows; K = the rows' capacity (a
+ *   multiple of 128).
  * lda, ldb multiples of 16, ldc of 8; any M, N, K (no multiple needed); M = 0
  * (moe_fp8_gemm) or K = 0 (moe_fp8_gemm_dw) are valid.
  */

@@ -18,7 +18,7 @@ def moe():
 def test_c_entries_refuse(moe):
     L = moe.lib()
     rows = lambda type=0, x=4096, ldx=256, r=8, c=200, swiglu=0, q=4096, ldq=208, s=4096, lds=8: (   # noqa: E731
-        L.moe_fp8_quantize_rows(type, x, ldx, r, c, None, None, swiglu, q, ldq, s, lds, None))
+        L.moe_fp8_quantize_rows(type, x, ldx, max(r, 0), r, c, None, None, swiglu, q, ldq, s, lds, None))
     assert rows(type=3) == 1 and rows(type=9) == 1           # codes are not quantized again
     assert rows(r=-1) == 1 and rows(c=0) == 1 and rows(swiglu=2) == 1
     assert rows(x=None) == 1 and rows(q=None) == 1 and rows(s=None) == 1
@@ -29,7 +29,7 @@ def test_c_entries_refuse(moe):
     assert rows(c=(1 << 20) + 1, ldx=1 << 21, ldq=1 << 21) == 2 and rows(r=1 << 31, lds=1 << 31) == 2
     assert rows(r=0, x=None) == 0
     cols = lambda x=4096, ldx=200, r=300, c=200, q=4096, ldq=304, lds=200: L.moe_fp8_quantize_cols(   # noqa: E731
-        0, x, ldx, r, c, None, None, q, ldq, 4096, lds, None)
+        0, x, ldx, r, r, c, None, None, q, ldq, 4096, lds, None)
     assert cols(ldq=288) == 1 and cols(lds=199) == 1 and cols(ldx=100) == 1 and cols(r=65536 * 128, ldq=1 << 24) == 2
     blocks = lambda E=2, K=100, N=64, tr=0, q=4096, ldq=112: L.moe_fp8_quantize_blocks(   # noqa: E731
         0, 4096, E, K, N, tr, q, ldq, 4096, None)

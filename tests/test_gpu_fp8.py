@@ -117,6 +117,63 @@ def test_gathered_rows_strides_and_what_is_left_alone():
 
 
 @pytest.mark.gpu
+def test_a_source_row_that_is_none_gives_zeros():
+    from fine_grained_mixture_top_b200 import moe
+    x = torch.randn(5, 160, device="cuda")
+    src = torch.tensor([4, 5, -1, 2 ** 31 - 1, -2 ** 31, 0, 1000000], dtype=torch.int32)
+    want = torch.where(((src >= 0) & (src < 5))[:, None], x.cpu()[src.clamp(0, 4).long()], torch.zeros(()))
+    q, s = moe.fp8_quantize_rows(x, row_src=src.cuda())
+    cq, cs = ref_blocks(want, 1, 128)
+    same(q, cq)
+    assert torch.equal(s.cpu(), cs.t())
+    q, s = moe.fp8_quantize_cols(x, row_src=src.cuda())
+    cq, cs = ref_blocks(want, 128, 1)
+    same(q, cq.t())
+    assert torch.equal(s.cpu(), cs)
+
+
+@pytest.mark.gpu
+def test_rows_past_32_bits_of_elements():
+    """Row tensors of more than 2^31 elements: the first, some in between and the
+    last rows of the gather, the quantizer, a product and the weighted sum."""
+    from fine_grained_mixture_top_b200 import moe
+    T, E, K, d = 42000, 3, 1, 64
+    W = 52224                     # 42000 x 52224 > 2^31 elements
+    idx = torch.randint(0, E, (T, K), dtype=torch.int32, device="cuda")
+    rt = moe.sort_pairs(idx, torch.ones(T, K, device="cuda"), E)
+    R = rt.struct.R_max
+    x = torch.zeros(T, W, dtype=torch.bfloat16, device="cuda")
+    x[:, ::1000] = torch.randn(T, 1, device="cuda").bfloat16()
+    x[:, -1] = 3.0
+    rows = moe.permute(rt, x)
+    tok = rt["row_tok"].long()
+    real = (tok >= 0).nonzero()[:, 0]
+    pick = real[torch.linspace(0, real.numel() - 1, 9).long().cuda()]
+    assert torch.equal(rows[pick], x[tok[pick]])
+    out = moe.unpermute(rt, rows)
+    assert torch.equal(out[-5:], x[-5:]) and torch.equal(out[:5], x[:5])
+    del out
+    q, s = moe.fp8_quantize_rows(x, row_src=rt["row_tok"], rows_used=rt["offsets"][-1:])
+    cq, cs = ref_blocks(x[tok[pick]].float().cpu(), 1, 128)
+    same(q[pick], cq)
+    assert torch.equal(s[:, pick].cpu(), cs.t())
+    del x, rows
+    b, sb = rand_codes((E, 72, W), 3), rand_scales((E, 1, W // 128), 4)
+    y = moe.fp8_gemm(q, s, b, sb, routing=rt)
+    del q
+    e = int(rt["tile_expert"][int(pick[-1]) // 128])
+    a = cq.cuda().view(E4M3)[-1:]
+    check(y[pick[-1:]], *block_sum(a, cs.t()[:, -1:].cuda(), b[e], by_col(sb[e], 72)))
+    a, sa = rand_codes((R, d), 5), rand_scales((1, R), 6)
+    b, sb = rand_codes((E, W - 3, d), 7), rand_scales((E, W // 128, 1), 8)
+    y = moe.fp8_gemm(a, sa, b, sb, routing=rt)      # more than 2^31 elements of C, ragged columns
+    assert y.shape[0] * y.stride(0) > 2 ** 31
+    for r in (int(pick[0]), int(pick[-1])):
+        e = int(rt["tile_expert"][r // 128])
+        check(y[r:r + 1], *block_sum(a[r:r + 1], sa[:, r:r + 1], b[e], by_col(sb[e], W - 3)))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("R,C", [(3, 128), (70, 200), (33, 77), (129, 1024)])
 def test_swiglu_then_quantize(R, C, dtype):
