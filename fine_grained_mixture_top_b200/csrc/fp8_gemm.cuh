@@ -30,8 +30,7 @@ struct Fp8Params {
   const float* sB;       // BROWS: [K / 128, ldsB]; else [planes, nb, kb]
   int64_t ldsA, ldsB, ldc;
   __nv_bfloat16* C;
-  const int* offsets;      // [E + 1] first row (GROUPED) or k (DW) of each expert, multiples of 128
-  const int* tile_expert;  // GROUPED: expert of each 128-row tile
+  const int* offsets;  // [E + 1] first row (GROUPED) or k (DW) of each expert, multiples of 128
   int E, M, N, nb, kb;     // nb, kb: 128-blocks of N and of the summed dimension
   int mode;
   int mt, nt;              // tiles of M (not GROUPED: from offsets) and N

@@ -531,7 +531,6 @@ static moe_status fp8_product(int mode, int64_t M, int64_t N, int64_t K, int32_t
   p.ldc = ldc;
   p.C = static_cast<__nv_bfloat16*>(C);
   p.offsets = rt ? rt->offsets : nullptr;
-  p.tile_expert = rt ? rt->tile_expert : nullptr;
   p.E = planes;
   p.M = (int)M;
   p.N = (int)N;
@@ -589,8 +588,7 @@ static moe_status fp8_product(int mode, int64_t M, int64_t N, int64_t K, int32_t
 static moe_status check_product(int64_t M, int64_t N, int64_t K, int32_t E, const moe_routing* rt, const void* A,
                                 int64_t lda, const float* sA, const void* B, int64_t ldb, const float* sB,
                                 const void* C, int64_t ldc) {
-  if (rt && (!rt->offsets || !rt->tile_expert || !aligned16(rt->offsets) || !aligned16(rt->tile_expert)))
-    return MOE_ERR_INVALID_ARG;
+  if (rt && (!rt->offsets || !aligned16(rt->offsets))) return MOE_ERR_INVALID_ARG;
   if (M >= (int64_t(1) << 31) - 256 || N >= (int64_t(1) << 31) - 256 || K >= (int64_t(1) << 31) - 256 || E > 1024 ||
       (!rt && E != 1))
     return MOE_ERR_UNSUPPORTED;

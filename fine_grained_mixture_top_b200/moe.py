@@ -324,7 +324,8 @@ def mx_quantize_cols(w, stream=None):
 
 # ----------------------------------------------------------------------------
 # Rows sorted by expert and back.  These check their tensors, allocate what the
-# caller leaves out, and run on the tensors' device.
+# caller leaves out, and run on the tensors' device, on `stream` or its current
+# stream.
 
 _torch = None
 _DTYPES = {}
@@ -377,22 +378,30 @@ def _matrix(t, name: str, rows: int, cols: int, device, dtype=None) -> int:
     return ld
 
 
-def _away(device) -> bool:
-    """Is `device` another than the current one?  (It then has to be made current for the call.)"""
+def _elsewhere(device, stream) -> bool:
+    """Does a call on tensors of `device` have to change the current device or
+    stream?  (It then runs with them current, so that what it allocates belongs
+    to the stream that uses it.)"""
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}: a CUDA device is needed")
-    return _torch._C._cuda_getDevice() != device.index
+    return stream is not None or _torch._C._cuda_getDevice() != device.index
 
 
-def _stream_on(stream, device) -> int:
-    """Handle of `stream`, or of the current stream of the (current) device
-    (without the Python object around it: 0.1 instead of 3.4 us)."""
-    return _torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-
-
-def _on(device, fn, *args, **kw):
+def _there(device, stream, fn, *args):
+    """fn(*args) with `device` and `stream` (or the device's current stream) current."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
     with _torch.cuda.device(device):
-        return fn(*args, **kw)
+        if stream is None:
+            return fn(*args)
+        with _torch.cuda.stream(stream):
+            return fn(*args)
+
+
+def _current(device) -> int:
+    """Handle of the (current) device's current stream (without the Python object
+    around it: 0.1 instead of 3.4 us)."""
+    return _torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=None, stream=None) -> Routing:
@@ -400,15 +409,15 @@ def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=N
     gates topk_gate [T, K] (fp32) by expert: see moe_sort_pairs in moe.h.  A
     Routing of an earlier call with the same T, K and E can be given again as
     `routing`; it is overwritten.  ws: a uint8 workspace of moe_sort_sizes'
-    bytes (default: allocated)."""
+    bytes (default: allocated); calls that may overlap need one each."""
     torch = _th()
     dev = topk_idx.device
     T, K = _shape2(topk_idx, "topk_idx")
     for t, name, dt in ((topk_idx, "topk_idx", torch.int32), (topk_gate, "topk_gate", torch.float32)):
         if _matrix(t, name, T, K, dev, dt) != K:
             raise ValueError(f"{name}: must be contiguous")
-    if _away(dev):
-        return _on(dev, sort_pairs, topk_idx, topk_gate, E, routing, ws, stream)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, sort_pairs, topk_idx, topk_gate, E, routing, ws)
     if routing is None or ws is None:
         P, R, need = c_int64(0), c_int64(0), ctypes.c_size_t(0)
         _check(lib().moe_sort_sizes(T, E, K, ctypes.byref(P), ctypes.byref(R), ctypes.byref(need)), "moe_sort_sizes")
@@ -434,7 +443,7 @@ def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=N
     r["topk_idx"], r["topk_gate"] = topk_idx, topk_gate
     st.topk_idx, st.topk_gate = _ptr(topk_idx), _ptr(topk_gate)
     _check(lib().moe_sort_pairs(T, E, K, ctypes.byref(st), _ptr(ws), 0 if ws is None else ws.numel(),
-                                _stream_on(stream, dev)), "moe_sort_pairs")
+                                _current(dev)), "moe_sort_pairs")
     return routing
 
 
@@ -454,15 +463,15 @@ def permute(routing: Routing, src, rows=None, stream=None):
     code = _dtype_code(src, "src", 3)
     width = _shape2(src, "src")[1]
     ld = _matrix(src, "src", T, width, dev)
-    if _away(dev):
-        return _on(dev, permute, routing, src, rows, stream)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, permute, routing, src, rows)
     ldr = width
     if rows is None:
         rows = src.new_empty((R, width))
     else:
         ldr = _matrix(rows, "rows", R, width, dev, src.dtype)
     _check(lib().moe_permute(T, E, ctypes.byref(routing.struct), code, width, _ptr(src), ld, _ptr(rows), ldr,
-                             _stream_on(stream, dev)), "moe_permute")
+                             _current(dev)), "moe_permute")
     return rows
 
 
@@ -472,15 +481,15 @@ def _sum_rows(fn, what, routing, rows, out, stream):
     code = _dtype_code(rows, "rows")
     width = _shape2(rows, "rows")[1]
     ld = _matrix(rows, "rows", R, width, dev)
-    if _away(dev):
-        return _on(dev, _sum_rows, fn, what, routing, rows, out, stream)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, _sum_rows, fn, what, routing, rows, out, None)
     ldo = width
     if out is None:
         out = rows.new_empty((T, width))
     else:
         ldo = _matrix(out, "out", T, width, dev, rows.dtype)
     _check(fn(T, E, ctypes.byref(routing.struct), code, width, _ptr(rows), ld, _ptr(out), ldo,
-              _stream_on(stream, dev)), what)
+              _current(dev)), what)
     return out
 
 
@@ -506,8 +515,12 @@ def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: b
     ld = _matrix(rows, "rows", R, width, dev)
     ldo = _matrix(dout, "dout", T, width, dev, rows.dtype)
     K = routing.tensors["topk_idx"].shape[1]
-    if _away(dev):
-        return _on(dev, unpermute_bwd, routing, dout, rows, drows, dgate, pairs, stream)
+    if not pairs and routing.struct.P_max != T * K:
+        raise ValueError("a routing with token rounding has no place per choice: pass pairs=True")
+    if drows is not None and drows.data_ptr() == rows.data_ptr() and drows.numel():
+        raise ValueError("drows: must not be rows")
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, unpermute_bwd, routing, dout, rows, drows, dgate, pairs)
     ldd = width
     if drows is None:
         drows = rows.new_empty((R, width))
@@ -522,7 +535,7 @@ def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: b
         raise ValueError(f"dgate: contiguous {shape} on {dev} expected")
     _check(lib().moe_unpermute_bwd(T, E, K, ctypes.byref(routing.struct), code, width, _ptr(dout), ldo, _ptr(rows),
                                    ld, _ptr(drows), ldd, _ptr(dgate) if pairs else None,
-                                   None if pairs else _ptr(dgate), _stream_on(stream, dev)), "moe_unpermute_bwd")
+                                   None if pairs else _ptr(dgate), _current(dev)), "moe_unpermute_bwd")
     return drows, dgate
 
 
@@ -570,8 +583,8 @@ def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
     rows = n_in if row_src is None else row_src.shape[0]
     src = _i32(row_src, "row_src", rows, dev)
     used = _i32(rows_used, "rows_used", 1, dev)
-    if _away(dev):
-        return _on(dev, _quantize, cols_form, x, row_src, rows_used, swiglu, codes, scales, stream)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, _quantize, cols_form, x, row_src, rows_used, swiglu, codes, scales, None)
     out, blocks = ((cols, rows), -(-rows // 128)) if cols_form else ((rows, cols), -(-cols // 128))
     ldc, lds = (out[1] + 15) // 16 * 16, out[0]
     if codes is None:
@@ -584,10 +597,10 @@ def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
         lds = _matrix(scales, "scales", blocks, lds, dev, torch.float32)
     if cols_form:
         _check(lib().moe_fp8_quantize_cols(code, _ptr(x), ld, n_in, rows, cols, src, used, _ptr(codes), ldc,
-                                           _ptr(scales), lds, _stream_on(stream, dev)), "moe_fp8_quantize_cols")
+                                           _ptr(scales), lds, _current(dev)), "moe_fp8_quantize_cols")
     else:
         _check(lib().moe_fp8_quantize_rows(code, _ptr(x), ld, n_in, rows, cols, src, used, 1 if swiglu else 0,
-                                           _ptr(codes), ldc, _ptr(scales), lds, _stream_on(stream, dev)),
+                                           _ptr(codes), ldc, _ptr(scales), lds, _current(dev)),
                "moe_fp8_quantize_rows")
     return codes, scales
 
@@ -619,8 +632,8 @@ def fp8_quantize_blocks(w, transpose: bool, codes=None, scales=None, stream=None
     dev = w.device
     K, N = w.shape[-2:]
     E = w.shape[0] if w.dim() == 3 else 1
-    if _away(dev):
-        return _on(dev, fp8_quantize_blocks, w, transpose, codes, scales, stream)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, fp8_quantize_blocks, w, transpose, codes, scales)
     a, b = (N, K) if transpose else (K, N)
     lead = w.shape[:-2]
     if codes is None:
@@ -633,7 +646,7 @@ def fp8_quantize_blocks(w, transpose: bool, codes=None, scales=None, stream=None
     if scales.dtype != torch.float32:
         raise TypeError(f"scales: {scales.dtype}, expected torch.float32")
     _check(lib().moe_fp8_quantize_blocks(code, _ptr(w), E, K, N, 1 if transpose else 0, _ptr(codes), ldc, _ptr(scales),
-                                         _stream_on(stream, dev)), "moe_fp8_quantize_blocks")
+                                         _current(dev)), "moe_fp8_quantize_blocks")
     return codes, scales
 
 
@@ -698,11 +711,11 @@ def fp8_gemm(a, sa, b, sb, routing: Routing | None = None, out=None, stream=None
         raise ValueError(f"sb: contiguous {(*lead, nb, kb)} on {dev} expected, got {tuple(sb.shape)}")
     if sb.dtype != torch.float32:
         raise TypeError(f"sb: {sb.dtype}, expected torch.float32")
-    if _away(dev):
-        return _on(dev, fp8_gemm, a, sa, b, sb, routing, out, stream)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, fp8_gemm, a, sa, b, sb, routing, out)
     out, ldo = _out(out, "out", (M, N), dev)
     _check(lib().moe_fp8_gemm(M, N, K, E, None if routing is None else ctypes.byref(routing.struct), _ptr(a), lda,
-                              _ptr(sa), lds, _ptr(b), ldb, _ptr(sb), _ptr(out), ldo, _stream_on(stream, dev)),
+                              _ptr(sa), lds, _ptr(b), ldb, _ptr(sb), _ptr(out), ldo, _current(dev)),
            "moe_fp8_gemm")
     return out
 
@@ -727,11 +740,11 @@ def fp8_gemm_dw(a, sa, b, sb, routing: Routing | None = None, out=None, stream=N
         lead = (E,)
         if K != R or rdev != dev:
             raise ValueError(f"a: {K} tokens on {dev}, expected the routing's {R} rows on {rdev}")
-    if _away(dev):
-        return _on(dev, fp8_gemm_dw, a, sa, b, sb, routing, out, stream)
+    if _elsewhere(dev, stream):
+        return _there(dev, stream, fp8_gemm_dw, a, sa, b, sb, routing, out)
     out, ldo = _out(out, "out", (*lead, M, N), dev)
     _check(lib().moe_fp8_gemm_dw(M, N, K, E, None if routing is None else ctypes.byref(routing.struct), _ptr(a), lda,
-                                 _ptr(sa), ldsa, _ptr(b), ldb, _ptr(sb), ldsb, _ptr(out), ldo, _stream_on(stream, dev)),
+                                 _ptr(sa), ldsa, _ptr(b), ldb, _ptr(sb), ldsb, _ptr(out), ldo, _current(dev)),
            "moe_fp8_gemm_dw")
     return out
 

@@ -276,6 +276,29 @@ def test_dense_product(M, N, K):
     assert moe.moe_get_status() == (0, 0)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(3, 40, 1), (40, 70, 129), (300, 600, 250), (5000, 1000, 131), (2500, 2500, 7)])
+def test_bytes_between_rows_count_for_nothing(M, N, K):
+    """Row strides are multiples of 16: what lies between a row's end and the next
+    row (here the NaN code) is not part of the product."""
+    from fine_grained_mixture_top_b200 import moe
+
+    def padded(rows, seed):
+        t = torch.full((rows, up(K, 16) + 16), 0x7F, dtype=torch.uint8, device="cuda").view(E4M3)[:, :K]
+        t.copy_(rand_codes((rows, K), seed))
+        return t
+    a, b = padded(M, 1), padded(N, 2)
+    kb = -(-K // 128)
+    sa, sb = rand_scales((kb, M), 3), rand_scales((-(-N // 128), kb), 4)
+    check(moe.fp8_gemm(a, sa, b, sb), *block_sum(a, sa, b, by_col(sb, N)))
+    sa, sb = rand_scales((kb, M), 5), rand_scales((kb, N), 6)
+    check(moe.fp8_gemm_dw(a, sa, b, sb), *block_sum(a, sa, b, sb))
+    x = torch.randn(M, K, device="cuda")
+    q, s = moe.fp8_quantize_rows(x)      # the quantizer's own padding is left as it was allocated
+    y = moe.fp8_gemm(q, s, b, sb := rand_scales((-(-N // 128), kb), 7))
+    check(y, *block_sum(q, s, b, by_col(sb, N)))
+
+
 GROUPED = [  # T, E, K, N, width, drop
     (1, 4, 1, 8, 16, 0.0), (5, 64, 4, 136, 128, 0.0), (300, 7, 3, 520, 640, 0.3), (2000, 5, 2, 264, 1000, 0.0),
     (130, 3, 2, 1000, 129, 0.9), (700, 16, 6, 384, 256, 0.1), (60, 9, 2, 72, 300, 1.0), (3000, 2, 1, 1544, 520, 0.0),

@@ -332,3 +332,37 @@ def test_nan_and_infinity_stay_in_their_rows():
     assert torch.equal(out[0], torch.full((16,), 2.0, device="cuda"))
     assert torch.isnan(out[1, 3]) and int(torch.isnan(out).sum()) == 1
     assert torch.all(out[2] == 0)
+
+
+@pytest.mark.gpu
+def test_a_stream_given_by_name_and_what_is_refused():
+    """With `stream` the whole call belongs to it, allocations too: work queued
+    before it on another stream is not waited for, memory it takes is not shared."""
+    from fine_grained_mixture_top_b200 import moe
+    T, E, K, width = 20000, 12, 3, 128
+    idx, gate = selection(T, E, K, 21, 0.1)
+    ti, tg = torch.from_numpy(idx).cuda(), torch.from_numpy(gate).cuda()
+    x = torch.randn(T, width, device="cuda")
+    ref = moe.unpermute(rt := moe.sort_pairs(ti, tg, E), moe.permute(rt, x))
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = []
+    for _ in range(20):
+        junk = torch.full((1 << 22,), 1, device="cuda")      # the current stream keeps taking and freeing memory
+        r = moe.sort_pairs(ti, tg, E, stream=s)
+        rows = moe.permute(r, x, stream=s)
+        outs.append(moe.unpermute(r, rows, stream=s))
+        del junk, r, rows
+    s.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    from workloads import MoEConfig, make_inputs
+    cfg = MoEConfig("rows2", T=64, d=128, E=4, n=64, K=2, seed=1)
+    layer = moe.MoELayer(cfg.T, cfg.d, cfg.E, cfg.n, cfg.K)
+    with pytest.raises(ValueError, match="sort_pairs"):
+        moe.sort_pairs(ti[:64, :2].contiguous(), tg[:64, :2].contiguous(), 4, routing=layer.routing)
+    with pytest.raises(ValueError, match="another"):
+        moe.sort_pairs(ti, tg, E + 1, routing=rt)
+    if torch.cuda.device_count() > 1:
+        with pytest.raises(ValueError, match="stream"):
+            moe.permute(rt, x, stream=torch.cuda.Stream(device=1))

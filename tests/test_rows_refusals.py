@@ -106,3 +106,9 @@ def test_binding_refuses(moe):
         moe.unpermute(rt, torch.zeros(1000, 16))
     with pytest.raises(TypeError, match="dout"):
         moe.unpermute_bwd(rt, x.half(), torch.zeros(1024, 16))
+    rows = torch.zeros(1024, 16)
+    with pytest.raises(ValueError, match="must not be rows"):
+        moe.unpermute_bwd(rt, x, rows, drows=rows)
+    rt.struct.P_max = 8 + 127 * 8        # capacities of token rounding
+    with pytest.raises(ValueError, match="pairs=True"):
+        moe.unpermute_bwd(rt, x, rows)
