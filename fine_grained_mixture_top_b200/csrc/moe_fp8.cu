@@ -378,6 +378,72 @@ cudaError_t launch_tiles(const QuantArgs& a, int E, const void* in, cudaStream_t
               : go(fp8_quant_tile_kernel<T, false, COLS, TRANS, false>);
 }
 
+// Copies of rows quantized once: codes[r] = from.codes[row_src[r]] and the same of
+// the scales, zeros (and the scale of zeros) where there is no such row.  A block
+// has blockDim.y kGatherRows rows, kGatherRows of them in flight per thread, in
+// 16-byte pieces of blockDim.x columns; blocks of the first column part take
+// their rows' scales.  (One row per thread and blocks for the scales: the
+// gather of 16384 tokens of 2048 values to 131072 rows took 137 us in all where
+// this takes 87, and quantizing every copied row 110.)
+constexpr int kGatherRows = 8;
+__global__ void __launch_bounds__(256) fp8_gather_kernel(const QuantArgs a, const uint8_t* __restrict__ codes,
+                                                         int64_t ld, const float* __restrict__ scales,
+                                                         int64_t ld_scales) {
+  pdl_wait();
+  const int64_t used = a.rows_used ? min((int64_t)__ldg(a.rows_used), a.rows) : a.rows;
+  const int per = blockDim.y * kGatherRows;
+  const int64_t r0 = (int64_t)blockIdx.x * per;
+  if (r0 >= used) return;
+  const int e0 = 16 * (int)(blockIdx.y * blockDim.x + threadIdx.x);
+  if (e0 < a.cols) {
+    int from[kGatherRows];
+    uint4 v[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      const int64_t r = r0 + i * blockDim.y + threadIdx.y;
+      from[i] = r < used ? __ldg(a.row_src + r) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if ((uint32_t)from[i] < (uint32_t)a.in_rows) v[i] = load16(codes + from[i] * ld + e0);
+    }
+    const int64_t step = (int64_t)blockDim.y * a.ld_codes;
+    uint8_t* out = a.codes + (r0 + threadIdx.y) * a.ld_codes + e0;
+    const int live = (int)min((int64_t)kGatherRows, (used - r0 - threadIdx.y + blockDim.y - 1) / blockDim.y);
+    if (e0 + 16 <= a.cols) {
+#pragma unroll
+      for (int i = 0; i < kGatherRows; ++i)
+        if (i < live) *reinterpret_cast<uint4*>(out + i * step) = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGatherRows; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (i < live && e0 + j < a.cols) out[i * step + j] = (uint8_t)(w[j / 4] >> (8 * (j % 4)));
+      }
+    }
+  }
+  if (blockIdx.y == 0) {  // a warp per block of columns, its lanes along the rows
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, warps = (blockDim.x * blockDim.y) >> 5;
+    for (int i = tid & 31; i < per && r0 + i < used; i += 32) {
+      const int from = __ldg(a.row_src + r0 + i);
+      const bool real = from >= 0 && from < a.in_rows;
+      for (int kb = tid >> 5; kb < a.kblocks; kb += warps)
+        a.scales[(int64_t)kb * a.ld_scales + r0 + i] =
+            real ? __ldg(scales + (int64_t)kb * ld_scales + from) : kAmaxFloor / kE4m3Max;
+    }
+  }
+}
+cudaError_t launch_gather(const QuantArgs& a, const QuantArgs& once, cudaStream_t s) {
+  const int64_t pieces = cdiv(a.cols, 16), parts = cdiv(pieces, 256);
+  const unsigned x = (unsigned)(cdiv(cdiv(pieces, parts), 32) * 32), y = 256 / x;
+  return launch_pdl(fp8_gather_kernel, dim3((unsigned)cdiv(a.rows, y * kGatherRows), (unsigned)cdiv(pieces, x)),
+                    dim3(x, y), 0, s, a, (const uint8_t*)once.codes, once.ld_codes, (const float*)once.scales,
+                    once.ld_scales);
+}
+
 int64_t elem_size(moe_dtype t) { return t == MOE_F32 ? 4 : (t == MOE_BF16 || t == MOE_F16) ? 2 : 0; }
 moe_status check_quant(moe_dtype type, const void* in, int64_t ld_in, int64_t width, const void* codes,
                        int64_t ld_codes, int64_t code_cols, const float* scales) {
@@ -410,8 +476,9 @@ using namespace moe;
 extern "C" {
 
 moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
-                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
-                                 int64_t ld_codes, float* scales, int64_t ld_scales, void* stream) {
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, int32_t swiglu,
+                                 void* codes, int64_t ld_codes, float* scales, int64_t ld_scales, void* ws,
+                                 size_t ws_bytes, void* stream) {
   ApiRange api_range("moe_fp8_quantize_rows");
   if (rows < 0 || in_rows < 0 || cols < 1 || swiglu < 0 || swiglu > 1) return MOE_ERR_INVALID_ARG;
   const int kb = (int)cdiv(cols, kBlk);
@@ -434,9 +501,34 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   a.codes = static_cast<uint8_t*>(codes);
   a.scales = scales;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t need = moe_fp8_gather_ws(in_rows, cols);
+  if (row_src && in_rows > 0 && rows >= 2 * in_rows && ws && ws_bytes >= need) {
+    if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    // each input row once into ws, then copies of its codes and scales
+    QuantArgs once = a;
+    once.rows = in_rows;
+    once.row_src = nullptr;
+    once.rows_used = nullptr;
+    once.ld_codes = cdiv(cols, 16) * 16;
+    once.codes = static_cast<uint8_t*>(ws);
+    once.ld_scales = in_rows;
+    once.scales = reinterpret_cast<float*>(once.codes + in_rows * once.ld_codes);
+    {
+      ProfScope ps(s, "fp8_quantize_rows");
+      MOE_BY_TYPE(type, (launch_rows<T>(once, in, swiglu != 0, s)));
+    }
+    ProfScope ps(s, "fp8_gather_codes");
+    MOE_TRY_CUDA(launch_gather(a, once, s));
+    return MOE_OK;
+  }
   ProfScope ps(s, "fp8_quantize_rows");
   MOE_BY_TYPE(type, (launch_rows<T>(a, in, swiglu != 0, s)));
   return MOE_OK;
+}
+
+size_t moe_fp8_gather_ws(int64_t in_rows, int32_t cols) {
+  if (in_rows < 0 || cols < 1) return 0;
+  return (size_t)in_rows * ((size_t)cdiv(cols, 16) * 16 + (size_t)cdiv(cols, kBlk) * sizeof(float));
 }
 
 moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,

@@ -104,7 +104,10 @@ def lib() -> ctypes.CDLL:
         L.moe_unpermute_bwd.argtypes = [c_int64, c_int32, c_int32, P(MoeRouting), c_int32, c_int64, c_void_p, c_int64,
                                         c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p]
         L.moe_fp8_quantize_rows.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int64, c_int32, c_void_p,
-                                            c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
+                                            c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                            ctypes.c_size_t, c_void_p]
+        L.moe_fp8_gather_ws.argtypes = [c_int64, c_int32]
+        L.moe_fp8_gather_ws.restype = ctypes.c_size_t
         L.moe_fp8_quantize_cols.argtypes = [c_int32, c_void_p, c_int64, c_int64, c_int64, c_int32, c_void_p,
                                             c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
         L.moe_fp8_quantize_blocks.argtypes = [c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
@@ -599,8 +602,12 @@ def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
         _check(lib().moe_fp8_quantize_cols(code, _ptr(x), ld, n_in, rows, cols, src, used, _ptr(codes), ldc,
                                            _ptr(scales), lds, _current(dev)), "moe_fp8_quantize_cols")
     else:
+        ws, need = None, 0
+        if src is not None and rows >= 2 * n_in > 0:  # rows that repeat are quantized once
+            need = lib().moe_fp8_gather_ws(n_in, cols)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
         _check(lib().moe_fp8_quantize_rows(code, _ptr(x), ld, n_in, rows, cols, src, used, 1 if swiglu else 0,
-                                           _ptr(codes), ldc, _ptr(scales), lds, _current(dev)),
+                                           _ptr(codes), ldc, _ptr(scales), lds, _ptr(ws), need, _current(dev)),
                "moe_fp8_quantize_rows")
     return codes, scales
 

@@ -394,7 +394,9 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
  *   one per row and 128 columns.  row_src (nullable, [rows]): row r holds
  *   in[row_src[r]], zeros where that is outside [0, in_rows), as -1 is (a
  *   routing's row_tok gathers the tokens into expert order); in_rows is not
- *   looked at without row_src.  rows_used (nullable, one device int): rows from
+ *   looked at without row_src.  ws (nullable): with row_src and ws_bytes of at
+ *   least moe_fp8_gather_ws(in_rows, cols), a gather that repeats rows
+ *   quantizes each once, into ws, and copies its codes; the result is the same.  rows_used (nullable, one device int): rows from
  *   *rows_used on are left as they were (a routing's offsets + E).  swiglu = 1:
  *   in[.., 2 cols], and silu(in[c]) * in[cols + c] is quantized.
  * moe_fp8_quantize_cols: the same input -> codes[cols, ld_codes] transposed
@@ -406,8 +408,10 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
  *   scales[E, ceil(N/128), ceil(K/128)].
  */
 moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
-                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, int32_t swiglu, void* codes,
-                                 int64_t ld_codes, float* scales, int64_t ld_scales, void* stream);
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, int32_t swiglu,
+                                 void* codes, int64_t ld_codes, float* scales, int64_t ld_scales, void* ws,
+                                 size_t ws_bytes, void* stream);
+size_t moe_fp8_gather_ws(int64_t in_rows, int32_t cols);
 moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
                                  int32_t cols, const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
                                  float* scales, int64_t ld_scales, void* stream);

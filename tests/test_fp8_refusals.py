@@ -18,7 +18,7 @@ def moe():
 def test_c_entries_refuse(moe):
     L = moe.lib()
     rows = lambda type=0, x=4096, ldx=256, r=8, c=200, swiglu=0, q=4096, ldq=208, s=4096, lds=8: (   # noqa: E731
-        L.moe_fp8_quantize_rows(type, x, ldx, max(r, 0), r, c, None, None, swiglu, q, ldq, s, lds, None))
+        L.moe_fp8_quantize_rows(type, x, ldx, max(r, 0), r, c, None, None, swiglu, q, ldq, s, lds, None, 0, None))
     assert rows(type=3) == 1 and rows(type=9) == 1           # codes are not quantized again
     assert rows(r=-1) == 1 and rows(c=0) == 1 and rows(swiglu=2) == 1
     assert rows(x=None) == 1 and rows(q=None) == 1 and rows(s=None) == 1

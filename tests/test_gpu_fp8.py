@@ -133,6 +133,29 @@ def test_a_source_row_that_is_none_gives_zeros():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,C,R,swiglu", [(1, 16, 7, False), (9, 130, 300, False), (50, 1000, 384, True),
+                                          (33, 4100, 129, False), (20, 8192, 200, False)])
+def test_repeated_rows_are_the_same_either_way(T, C, R, swiglu):
+    """A gather that repeats rows quantizes each once and copies the codes: the
+    same bits as row by row (a gather of fewer rows than twice the input's)."""
+    from fine_grained_mixture_top_b200 import moe
+    x = data(T, C * (2 if swiglu else 1), torch.bfloat16, T).clamp_(-30, 30).cuda()
+    src = torch.randint(-1, T, (R,), dtype=torch.int32, generator=torch.Generator().manual_seed(T)).cuda()
+    used = torch.tensor([R - R // 4], dtype=torch.int32, device="cuda")
+    store = torch.full((R, up(C, 16) + 16), 1.5, device="cuda").to(E4M3)
+    scales = torch.full((-(-C // 128), R), 9.0, device="cuda")
+    moe.fp8_quantize_rows(x, row_src=src, rows_used=used, swiglu=swiglu, codes=store[:, :C], scales=scales)
+    n = int(used)
+    one, parts = max(1, 2 * T - 1), []
+    for r in range(0, n, one):
+        parts.append(moe.fp8_quantize_rows(x, row_src=src[r:min(n, r + one)].contiguous(), swiglu=swiglu))
+    assert torch.equal(store[:n, :C].contiguous().view(torch.uint8), torch.cat([p[0].contiguous().view(torch.uint8) for p in parts]))
+    assert torch.equal(scales[:, :n], torch.cat([p[1] for p in parts], 1))
+    assert torch.all(store[n:].float() == 1.5) and torch.all(store[:, C:].float() == 1.5)
+    assert torch.all(scales[:, n:] == 9.0)
+
+
+@pytest.mark.gpu
 def test_rows_past_32_bits_of_elements():
     """Row tensors of more than 2^31 elements: the first, some in between and the
     last rows of the gather, the quantizer, a product and the weighted sum."""
