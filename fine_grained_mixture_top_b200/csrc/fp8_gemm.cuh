@@ -251,14 +251,23 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// After a wait has run out no barrier tells when the copies and MMAs already
+// issued are done.  They need microseconds: a CTA that has given up stays for
+// 2^18 clocks, some 140 us, before it frees its TMEM and leaves.
+__device__ __forceinline__ void settle(const volatile int* abort_flag) {
+  if (*abort_flag == 0) return;
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1 << 18)) __nanosleep(1000);
+}
+
 // ----------------------------------------------------------------- few rows
 // The product with its operands exchanged, for few rows of A: the weights are
 // the MMA's 128 rows and up to 128 rows of A ("tokens", 32 at a time) its
 // columns, so that a tile of few tokens costs few columns in the tensor core, in
 // TMEM and in the epilogue, and reads the weights at the rate of memory.
 //
-// Dense products only: tiles of 128 columns of C x 32 tok_boxes tokens.  Where
-// there are fewer tiles than SMs, a cluster of `split` CTAs shares one, each
+// Dense products only: tiles of 128 columns of C x 32 tok_boxes tokens, at most
+// one per SM.  Where there are fewer than half as many, a cluster of `split` CTAs shares one, each
 // summing its share of the blocks; their fp32 sums meet in distributed shared
 // memory and are added in rank order.
 //
@@ -297,20 +306,6 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-// Barrier of the eight epilogue warps; true in all of them if any passes true.
-__device__ __forceinline__ bool epilogue_any(bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 q, %1, 0;\n\t"
-      "barrier.cta.red.or.pred p, 1, 256, q;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)x)
-      : "memory");
-  return r != 0;
-}
-
 // acc += 32 columns of a block's sums times their factors in shared memory.
 __device__ __forceinline__ void add_scaled(float* acc, const uint32_t (&v)[32], const float* factors) {
 #pragma unroll
@@ -336,18 +331,17 @@ __device__ __forceinline__ Fp8SmallTile fp8_small_tile(const Fp8Params& p, int i
 }
 
 // The tile's sums (from RANKS CTAs' shared memory at address `at` of each,
-// [token][128]) rounded and stored by `threads` threads of each of the CTAs; a
-// thread takes four columns of a token, and has all loads of several such
+// [token][128]) rounded and stored by all threads of each of the CTAs; a thread takes four columns of a token, and has all loads of several such
 // pieces in flight (one after the other they cost 4 us of a 7 us product).
 template <int RANKS>
 __device__ __forceinline__ void fp8_small_store(const Fp8Params& p, const Fp8SmallTile& t, uint32_t at, int rank,
-                                                int tid, int threads) {
+                                                int tid) {
   constexpr int U = RANKS >= 8 ? 1 : (RANKS >= 4 ? 2 : 4);
-  const int n_pieces = t.rows * 32, stride = RANKS * threads;
+  const int n_pieces = t.rows * 32, stride = RANKS * Fp8SmallShape::kThreads;
   uint32_t from[RANKS];
 #pragma unroll
   for (int r = 0; r < RANKS; ++r) from[r] = mapa_shared(at, r);
-  for (int i0 = rank * threads + tid; i0 < n_pieces; i0 += U * stride) {
+  for (int i0 = rank * Fp8SmallShape::kThreads + tid; i0 < n_pieces; i0 += U * stride) {
     float4 x[U][RANKS];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -426,58 +420,45 @@ __global__ void __maxnreg__((Fp8SmallShape::kMaxReg)) fp8_gemm_small_kernel(cons
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
 
-  const int tiles = p.mt * p.nt;
-  const int first = (int)blockIdx.x / split, step = (int)gridDim.x / split;
+  const Fp8SmallTile t = fp8_small_tile(p, (int)blockIdx.x / split);
   // this CTA's share of the blocks
   const int kb0 = (int)((int64_t)p.kb * rank / split), nkb = (int)((int64_t)p.kb * (rank + 1) / split) - kb0;
 
   if (warp == 0) {
     int s = 0;
     uint32_t phase = 1;
-    bool ok = true;
-    for (int id = first; id < tiles && ok; id += step) {
-      const Fp8SmallTile t = fp8_small_tile(p, id);
-      for (int kb = kb0; kb < kb0 + nkb; ++kb) {
-        if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, p.st, 0x381)) {
-          ok = false;
-          break;
-        }
-        if (elect_one()) {
-          const uint32_t bar = smem_u32(&full[s]), dst = base + s * stage;
-          mbar_arrive_expect_tx(bar, (uint32_t)stage);
-          tma_load_3d(dst, &p.tmA, bar, kb * kFp8Bk, t.n0, 0);
-          tma_load_3d(dst + kFp8Box, &p.tmB, bar, kb * kFp8Bk, t.m0, 0);
-        }
-        __syncwarp();
-        if (++s == S) s = 0, phase ^= 1;
+    for (int kb = kb0; kb < kb0 + nkb; ++kb) {
+      if (!mbar_wait(smem_u32(&empty[s]), phase, abort_flag, p.st, 0x381)) break;
+      if (elect_one()) {
+        const uint32_t bar = smem_u32(&full[s]), dst = base + s * stage;
+        mbar_arrive_expect_tx(bar, (uint32_t)stage);
+        tma_load_3d(dst, &p.tmA, bar, kb * kFp8Bk, t.n0, 0);
+        tma_load_3d(dst + kFp8Box, &p.tmB, bar, kb * kFp8Bk, t.m0, 0);
       }
+      __syncwarp();
+      if (++s == S) s = 0, phase ^= 1;
     }
   } else if (warp == 1) {
-    int s = 0, it = 0;
+    int s = 0;
     uint32_t phase = 0;
-    bool ok = true;
     const uint32_t idesc = idesc_f8(32 * p.tok_boxes, 128);
-    for (int id = first; id < tiles && ok; id += step) {
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int b = it % SH::kSlots;
-        if (!mbar_wait(smem_u32(&slot_empty[b]), ((it / SH::kSlots) & 1) ^ 1, abort_flag, p.st, 0x383) ||
-            !mbar_wait(smem_u32(&full[s]), phase, abort_flag, p.st, 0x382)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t a_s = base + s * stage;
-          const uint64_t ad = smem_desc_sw128(a_s, 16, 1024), bd = smem_desc_sw128(a_s + kFp8Box, 16, 1024);
+    for (int kb = 0; kb < nkb; ++kb) {
+      const int b = kb % SH::kSlots;
+      if (!mbar_wait(smem_u32(&slot_empty[b]), ((kb / SH::kSlots) & 1) ^ 1, abort_flag, p.st, 0x383) ||
+          !mbar_wait(smem_u32(&full[s]), phase, abort_flag, p.st, 0x382))
+        break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t a_s = base + s * stage;
+        const uint64_t ad = smem_desc_sw128(a_s, 16, 1024), bd = smem_desc_sw128(a_s + kFp8Box, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < kFp8Bk / 32; ++kk)
-            tc_mma_f8(tmem + b * 128, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-          tc_commit(smem_u32(&slot_full[b]));
-          tc_commit(smem_u32(&empty[s]));
-        }
-        __syncwarp();
-        if (++s == S) s = 0, phase ^= 1;
+        for (int kk = 0; kk < kFp8Bk / 32; ++kk)
+          tc_mma_f8(tmem + b * 128, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+        tc_commit(smem_u32(&slot_full[b]));
+        tc_commit(smem_u32(&empty[s]));
       }
+      __syncwarp();
+      if (++s == S) s = 0, phase ^= 1;
     }
   } else {
     const int ew = warp - 2;
@@ -486,80 +467,65 @@ __global__ void __maxnreg__((Fp8SmallShape::kMaxReg)) fp8_gemm_small_kernel(cons
     const uint32_t tq = tmem + ((uint32_t)(q * 32) << 16) + 32 * g;
     float* cs = reinterpret_cast<float*>(smem + scale_offset + ew * SH::kScaleWarp);
     float* sums = reinterpret_cast<float*>(smem + sum_offset);
-    int it = 0;
-    bool ok = true;
-    for (int id = first; id < tiles && ok; id += step) {
-      const Fp8SmallTile t = fp8_small_tile(p, id);
-      const float* sb_p = p.sB + (int64_t)(t.n0 / 128) * p.kb + kb0;
-      const float* sa_p = p.sA + (int64_t)kb0 * p.ldsA + t.m0 + 32 * g + lane;
-      const int left = p.M - (t.m0 + 32 * g + lane);
-      // a block's factors: the weights' block scale times this lane's tokens' scales
-      float sb = 0.f, sa0 = 0.f, sa1 = 0.f;
-      auto load_scales = [&] {
-        sb = load_now(sb_p);
-        sa0 = left > 0 ? load_now(sa_p) : 0.f;
-        sa1 = left > 64 ? load_now(sa_p + 64) : 0.f;
-        ++sb_p;
-        sa_p += p.ldsA;
-      };
-      auto take_scales = [&](int kb) {
-        float* f = cs + (kb & 1) * 64;
-        f[lane] = sa0 * sb;
-        f[32 + lane] = sa1 * sb;
-        __syncwarp();
-      };
-      float acc[64];
+    const float* sb_p = p.sB + (int64_t)(t.n0 / 128) * p.kb + kb0;
+    const float* sa_p = p.sA + (int64_t)kb0 * p.ldsA + t.m0 + 32 * g + lane;
+    const int left = p.M - (t.m0 + 32 * g + lane);
+    // a block's factors: the weights' block scale times this lane's tokens' scales
+    float sb = 0.f, sa0 = 0.f, sa1 = 0.f;
+    auto load_scales = [&] {
+      sb = load_now(sb_p);
+      sa0 = left > 0 ? load_now(sa_p) : 0.f;
+      sa1 = left > 64 ? load_now(sa_p + 64) : 0.f;
+      ++sb_p;
+      sa_p += p.ldsA;
+    };
+    auto take_scales = [&](int kb) {
+      float* f = cs + (kb & 1) * 64;
+      f[lane] = sa0 * sb;
+      f[32 + lane] = sa1 * sb;
+      __syncwarp();
+    };
+    float acc[64];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-      load_scales();
-      take_scales(0);
-      if (nkb > 1) load_scales();
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int b = it % SH::kSlots;
-        if (!mbar_wait(smem_u32(&slot_full[b]), (it / SH::kSlots) & 1, abort_flag, p.st, 0x384)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t v0[32], v1[32];
-        // (columns past the tile's tokens hold leftovers, whose sums are not stored)
-        tmem_ld32(tq + b * 128, v0);
-        tmem_ld32(tq + b * 128 + 64, v1);
-        if (kb + 1 < nkb) take_scales(kb + 1);
-        if (kb + 2 < nkb) load_scales();
-        tc_wait_ld_pair(v0, v1);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&slot_empty[b]));
-        const float* f = cs + (kb & 1) * 64;
-        add_scaled(acc, v0, f);
-        add_scaled(acc + 32, v1, f + 32);
-      }
+    for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+    load_scales();
+    take_scales(0);
+    if (nkb > 1) load_scales();
+    for (int kb = 0; kb < nkb; ++kb) {
+      const int b = kb % SH::kSlots;
+      if (!mbar_wait(smem_u32(&slot_full[b]), (kb / SH::kSlots) & 1, abort_flag, p.st, 0x384)) break;
+      tc_fence_after();
+      uint32_t v0[32], v1[32];
+      // (columns past the tile's tokens hold leftovers, whose sums are not stored)
+      tmem_ld32(tq + b * 128, v0);
+      tmem_ld32(tq + b * 128 + 64, v1);
+      if (kb + 1 < nkb) take_scales(kb + 1);
+      if (kb + 2 < nkb) load_scales();
+      tc_wait_ld_pair(v0, v1);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&slot_empty[b]));
+      const float* f = cs + (kb & 1) * 64;
+      add_scaled(acc, v0, f);
+      add_scaled(acc + 32, v1, f + 32);
+    }
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const int m = (i < 32 ? 32 * g : 64 + 32 * g - 32) + i;
-        if (m < t.rows) sums[m * 128 + q * 32 + lane] = acc[i];
-      }
-      if (split == 1) {
-        // a warp that has given up comes this far too, and the barriers tell the
-        // others: all leave after the same tile
-        epilogue_any(!ok);
-        if (ok) fp8_small_store<1>(p, t, base + sum_offset, 0, threadIdx.x - 64, 32 * SH::kEpi);
-        if (epilogue_any(!ok)) break;
-      }
+    for (int i = 0; i < 64; ++i) {
+      const int m = (i < 32 ? 32 * g : 64 + 32 * g - 32) + i;
+      if (m < t.rows) sums[m * 128 + q * 32 + lane] = acc[i];
     }
   }
 
+  settle(abort_flag);
   tc_fence_before();
   __syncthreads();
-  if (split > 1) {  // one tile per cluster
-    cluster_sync();
-    const Fp8SmallTile t = fp8_small_tile(p, first);
-    if (split == 2) fp8_small_store<2>(p, t, base + sum_offset, rank, threadIdx.x, SH::kThreads);
-    else if (split == 4) fp8_small_store<4>(p, t, base + sum_offset, rank, threadIdx.x, SH::kThreads);
-    else fp8_small_store<8>(p, t, base + sum_offset, rank, threadIdx.x, SH::kThreads);
-    cluster_sync();  // the other CTAs have read this one's sums
-  }
+  if (split > 1) cluster_sync();
+  const uint32_t at = base + sum_offset;
+  if (split == 1) fp8_small_store<1>(p, t, at, 0, threadIdx.x);
+  else if (split == 2) fp8_small_store<2>(p, t, at, rank, threadIdx.x);
+  else if (split == 4) fp8_small_store<4>(p, t, at, rank, threadIdx.x);
+  else fp8_small_store<8>(p, t, at, rank, threadIdx.x);
+  if (split > 1) cluster_sync();  // the other CTAs have read this one's sums
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -912,6 +878,7 @@ __global__ void __launch_bounds__(Fp8PairShape::kThreads, 1) __cluster_dims__(2,
     if (lane == 0) bulk_wait_all();
   }
 
+  settle(abort_flag);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // no CTA leaves while its pair may still arrive on its barriers

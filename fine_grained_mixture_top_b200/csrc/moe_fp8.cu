@@ -632,28 +632,28 @@ static moe_status fp8_product(int mode, int64_t M, int64_t N, int64_t K, int32_t
   p.st = DevStatus{dev.status, dev.spin_limit};
   const uint64_t bplanes = mode == FP8_GROUPED ? planes : 1, cplanes = dw ? planes : 1;
   const uint64_t bplane = (uint64_t)N * ldb;
-  // Pair tiles where they fill the machine, else tiles of 128 columns with the
-  // operands exchanged, of which the machine holds twice as many and which may
-  // share their sums (microseconds, pair tiles / exchanged: 16 x 4096 x 7168 28 /
-  // 13; 256 x 4096 x 7168, 16 pair tiles, 33 / 20; 1001 x 1528 x 2000, 24 pair
-  // tiles, 12.7 / 11.3; 2048 x 2048 x 2048, 64, 13 / 19).  Grouped products always
-  // take pairs: even with a few rows per expert they read the weights faster
+  // With at most one tile per SM of 128 columns and up to 128 rows: those, with the
+  // operands exchanged, of which the machine holds twice as many and which may share
+  // their sums (microseconds, pair tiles / exchanged: 16 x 4096 x 7168 28 / 13;
+  // 16 x 16384 x 7168, 128 tiles, 31 / 27; 1024 x 2048 x 7168, 128 tiles, 37 / 32;
+  // 1001 x 1528 x 2000, 96 tiles, 12.7 / 11.3).  With more, pairs: 1280 x 2048 x 1024,
+  // 160 tiles, 8.9 / 11.7; 2048 x 2048 x 2048, 256 tiles, 13 / 19.  Grouped products
+  // always take pairs: even with a few rows per expert they read the weights faster
   // (64 tokens x 8 of 128 experts, 1536 x 2048: 118 / 133).
-  const bool few = mode == FP8_DENSE && cdiv(M, 256) * cdiv(N, 256) < dev.sms / 4;
+  const int64_t tok_boxes = std::min<int64_t>(4, cdiv(M, 32));
+  const bool few = mode == FP8_DENSE && cdiv(M, 32 * tok_boxes) * cdiv(N, 128) <= dev.sms;
   if (few) {
-    p.tok_boxes = (int)std::min<int64_t>(4, cdiv(M, 32));
+    p.tok_boxes = (int)tok_boxes;
     if (!api_tensor_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, bplanes, N, K, ldb, bplane, 128, 128) ||
         !api_tensor_map(&p.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, 1, M, K, lda, (uint64_t)M * lda, 32 * p.tok_boxes, 128))
       return MOE_ERR_INVALID_ARG;
     p.mt = (int)cdiv(M, 32 * p.tok_boxes);
     p.nt = p.nb;
-    const int64_t tiles = (int64_t)p.mt * p.nt;
-    if (tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    const int tiles = p.mt * p.nt;
     p.split = 1;
     while (p.split < 8 && 2 * tiles * p.split <= dev.sms && p.kb >= 4 * p.split) p.split *= 2;
-    const int grid = p.split > 1 ? (int)tiles * p.split : (int)std::min<int64_t>(tiles, dev.sms);
     ProfScope ps(s, "fp8_gemm");
-    MOE_TRY_CUDA(launch_small(p, grid, Fp8SmallShape::smem(p.tok_boxes), s));
+    MOE_TRY_CUDA(launch_small(p, tiles * p.split, Fp8SmallShape::smem(p.tok_boxes), s));
     return MOE_OK;
   }
   if (!api_tensor_map(&p.tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, A, 1, M, K, lda, (uint64_t)M * lda, 128, 128) ||

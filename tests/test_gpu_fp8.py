@@ -277,7 +277,9 @@ def by_col(sb, N):
 
 DENSE = [(1, 1, 1), (1, 8, 16), (2, 136, 128), (128, 128, 128), (129, 130, 131), (16, 512, 7168), (300, 1000, 257),
          (1, 4096, 2000), (64, 72, 4096), (1000, 264, 640), (40, 2100, 1100), (2500, 520, 384), (33, 129, 8192),
-         (700, 700, 700), (257, 257, 129), (4100, 2056, 256)]
+         (700, 700, 700), (257, 257, 129), (4100, 2056, 256),
+         # either side of a tile of 128 x 128 per SM
+         (16, 16392, 300), (128, 18944, 128), (600, 3700, 129), (600, 3850, 129), (1280, 2040, 131), (257, 8200, 640)]
 
 
 @pytest.mark.gpu
