@@ -331,8 +331,9 @@ __device__ __forceinline__ Fp8SmallTile fp8_small_tile(const Fp8Params& p, int i
 }
 
 // The tile's sums (from RANKS CTAs' shared memory at address `at` of each,
-// [token][128]) rounded and stored by all threads of each of the CTAs; a thread takes four columns of a token, and has all loads of several such
-// pieces in flight (one after the other they cost 4 us of a 7 us product).
+// [token][128]) rounded and stored by all threads of each of the CTAs; a
+// thread takes four columns of a token, and has all loads of several such pieces
+// in flight (one after the other they cost 4 us of a 7 us product).
 template <int RANKS>
 __device__ __forceinline__ void fp8_small_store(const Fp8Params& p, const Fp8SmallTile& t, uint32_t at, int rank,
                                                 int tid) {

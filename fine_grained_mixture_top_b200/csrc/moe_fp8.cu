@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const QuantArgs a, 
 template <typename T, bool FAST, bool COLS>
 constexpr int kTileBlocks = sizeof(T) == 4 ? 3 : COLS ? 4 : FAST ? 5 : 6;
 template <typename T, bool FAST, bool COLS, bool TRANS, bool GATHER>
-__global__ void __launch_bounds__(256, kTileBlocks<T, FAST, COLS>) fp8_quant_tile_kernel(const QuantArgs a, const T* __restrict__ in0) {
+__global__ void __launch_bounds__(256, kTileBlocks<T, FAST, COLS>) fp8_quant_tile_kernel(const QuantArgs a,
+                                                                                           const T* __restrict__ in0) {
   pdl_wait();
   __shared__ uint32_t words[TRANS ? kBlk * 33 : 1];  // [column][4-row group], one word of padding
   __shared__ float part[8][COLS ? kBlk : 1];
@@ -532,8 +533,8 @@ size_t moe_fp8_gather_ws(int64_t in_rows, int32_t cols) {
 }
 
 moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
-                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
-                                 float* scales, int64_t ld_scales, void* stream) {
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, void* codes,
+                                 int64_t ld_codes, float* scales, int64_t ld_scales, void* stream) {
   ApiRange api_range("moe_fp8_quantize_cols");
   if (rows < 0 || in_rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
   if (cols > (1 << 20) || cdiv(rows, kBlk) > 65535) return MOE_ERR_UNSUPPORTED;

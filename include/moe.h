@@ -396,9 +396,10 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
  *   routing's row_tok gathers the tokens into expert order); in_rows is not
  *   looked at without row_src.  ws (nullable): with row_src and ws_bytes of at
  *   least moe_fp8_gather_ws(in_rows, cols), a gather that repeats rows
- *   quantizes each once, into ws, and copies its codes; the result is the same.  rows_used (nullable, one device int): rows from
- *   *rows_used on are left as they were (a routing's offsets + E).  swiglu = 1:
- *   in[.., 2 cols], and silu(in[c]) * in[cols + c] is quantized.
+ *   quantizes each once, into ws, and copies its codes; the result is the same.
+ *   rows_used (nullable, one device int): rows from *rows_used on are left as
+ *   they were (a routing's offsets + E).  swiglu = 1: in[.., 2 cols], and
+ *   silu(in[c]) * in[cols + c] is quantized.
  * moe_fp8_quantize_cols: the same input -> codes[cols, ld_codes] transposed
  *   (ld_codes >= rows), scales[ceil(rows / 128), ld_scales] (ld_scales >= cols):
  *   one per column and 128 rows, for products summed over the rows.
@@ -413,8 +414,8 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
                                  size_t ws_bytes, void* stream);
 size_t moe_fp8_gather_ws(int64_t in_rows, int32_t cols);
 moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, int64_t in_rows, int64_t rows,
-                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, void* codes, int64_t ld_codes,
-                                 float* scales, int64_t ld_scales, void* stream);
+                                 int32_t cols, const int32_t* row_src, const int32_t* rows_used, void* codes,
+                                 int64_t ld_codes, float* scales, int64_t ld_scales, void* stream);
 moe_status moe_fp8_quantize_blocks(moe_dtype type, const void* in, int32_t E, int32_t K, int32_t N, int32_t transpose,
                                    void* codes, int64_t ld_codes, float* scales, void* stream);
 
