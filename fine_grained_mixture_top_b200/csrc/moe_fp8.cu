@@ -503,7 +503,7 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   a.scales = scales;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t need = moe_fp8_gather_ws(in_rows, cols);
-  if (row_src && in_rows > 0 && rows >= 2 * in_rows && ws && ws_bytes >= need) {
+  if (row_src && in_rows > 0 && rows >= in_rows && ws && ws_bytes >= need) {
     if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
     // each input row once into ws, then copies of its codes and scales
     QuantArgs once = a;

@@ -603,7 +603,11 @@ def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
                                            _ptr(scales), lds, _current(dev)), "moe_fp8_quantize_cols")
     else:
         ws, need = None, 0
-        if src is not None and rows >= 2 * n_in > 0:  # rows that repeat are quantized once
+        # Rows that repeat often are quantized once and their codes copied (us, row by
+        # row / once: 32 x 7168 to 32768 rows 57 / 29, 4096 x 7168 to 65280 128 / 94);
+        # not with few repeats (4096 x 7168 to 16384: 34 / 38) or little to copy
+        # (1 x 2048 to 1024: 2.1 / 3.8, to 8192: 5.1 / 5.4).
+        if src is not None and rows >= 6 * n_in > 0 and rows * cols > 1 << 24:
             need = lib().moe_fp8_gather_ws(n_in, cols)
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
         _check(lib().moe_fp8_quantize_rows(code, _ptr(x), ld, n_in, rows, cols, src, used, 1 if swiglu else 0,

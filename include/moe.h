@@ -395,8 +395,11 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
  *   in[row_src[r]], zeros where that is outside [0, in_rows), as -1 is (a
  *   routing's row_tok gathers the tokens into expert order); in_rows is not
  *   looked at without row_src.  ws (nullable): with row_src and ws_bytes of at
- *   least moe_fp8_gather_ws(in_rows, cols), a gather that repeats rows
- *   quantizes each once, into ws, and copies its codes; the result is the same.
+ *   least moe_fp8_gather_ws(in_rows, cols), a gather of at least in_rows rows
+ *   quantizes each input row once, into ws, and copies its codes: the same
+ *   result, faster where rows repeat often (16384 rows of 2048 bf16 values
+ *   gathered 8 times: 85 us instead of 96; twice, 12.2 instead of 9.6 us for
+ *   4096 rows).
  *   rows_used (nullable, one device int): rows from *rows_used on are left as
  *   they were (a routing's offsets + E).  swiglu = 1: in[.., 2 cols], and
  *   silu(in[c]) * in[cols + c] is quantized.

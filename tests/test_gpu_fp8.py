@@ -156,6 +156,28 @@ def test_repeated_rows_are_the_same_either_way(T, C, R, swiglu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,C,R,swiglu", [(1, 16, 7, False), (9, 130, 300, False), (50, 1000, 384, True), (7, 33, 7, False),
+                                          (33, 4100, 129, False), (20, 8192, 200, False), (3, 7168, 2600, False)])
+def test_repeated_rows_with_a_workspace(T, C, R, swiglu):
+    """The workspace makes a gather quantize each row once: the same bits as without."""
+    from fine_grained_mixture_top_b200 import moe
+    x = data(T, C * (2 if swiglu else 1), torch.bfloat16, T).clamp_(-30, 30).cuda()
+    src = torch.randint(-1, T + 1, (R,), dtype=torch.int32, generator=torch.Generator().manual_seed(T)).cuda()
+    used = torch.tensor([R - R // 4], dtype=torch.int32, device="cuda")
+    need = moe.lib().moe_fp8_gather_ws(T, C)
+    got = []
+    for n in (0, need):
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        codes = torch.full((R, up(C, 16) + 16), 1.5, device="cuda").to(E4M3)
+        scales = torch.full((-(-C // 128), R), 9.0, device="cuda")
+        moe._check(moe.lib().moe_fp8_quantize_rows(
+            0, moe._ptr(x), x.shape[1], T, R, C, moe._ptr(src), moe._ptr(used), 1 if swiglu else 0, moe._ptr(codes),
+            codes.shape[1], moe._ptr(scales), R, moe._ptr(ws) if n else None, n, moe._current(x.device)), "rows")
+        got.append((codes.view(torch.uint8), scales))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.gpu
 def test_rows_past_32_bits_of_elements():
     """Row tensors of more than 2^31 elements: the first, some in between and the
     last rows of the gather, the quantizer, a product and the weighted sum."""
