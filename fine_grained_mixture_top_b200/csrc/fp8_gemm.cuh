@@ -193,17 +193,20 @@ struct BlockScales {
   }
 };
 
-// This thread's row of 128 columns from n on, rounded to bf16, into C: 64
-// columns at a time through this warp's staging buffer(s) at stg (a box is 32
-// rows x 128 bytes).
-template <int BUFS>
+// This thread's row of 128 columns from n0 on, rounded to bf16, into C: 64
+// columns at a time through this warp's two staging buffers at stg (a box is 32
+// rows x 128 bytes).  Nothing is staged before the tensor stores of the tile
+// before have left both buffers; a box past the last column is not staged.
 __device__ __forceinline__ void store_row(const Fp8Params& p, const float (&acc)[128], uint32_t stg, int plane,
                                           int row0, int n0) {
   const int lane = threadIdx.x & 31;
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int n = n0 + 64 * x;
-    if (n < p.N && n + 64 > p.N && p.N % 8 != 0) {
+    if (n >= p.N) continue;
+    if (n + 64 > p.N && p.N % 8 != 0) {
       // a tensor store is clipped to whole 16-byte chunks: the box with a
       // ragged last chunk goes element by element
       const int r = row0 + lane;
@@ -215,11 +218,7 @@ __device__ __forceinline__ void store_row(const Fp8Params& p, const float (&acc)
       }
       continue;
     }
-    const uint32_t buf = stg + (x % BUFS) * 4096;
-    if (BUFS == 1 || x == 0) {  // earlier stores have left the buffer(s)
-      if (lane == 0) bulk_wait_read<0>();
-      __syncwarp();
-    }
+    const uint32_t buf = stg + x * 4096;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float* a = acc + x * 64 + j * 8;
@@ -228,7 +227,7 @@ __device__ __forceinline__ void store_row(const Fp8Params& p, const float (&acc)
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && row0 < p.M && n < p.N) {
+    if (lane == 0 && row0 < p.M) {
       tma_store_3d(&p.tmC, buf, n, row0, plane);
       bulk_commit();
     }
@@ -874,7 +873,7 @@ __global__ void __launch_bounds__(Fp8PairShape::kThreads, 1) __cluster_dims__(2,
       if (!ok) break;
       const int then = fp8_turn(p, r + 1, pair, npairs);
       if (then < tiles) take_tile(then);
-      if (mine) store_row<2>(p, acc, stg, plane, row0, n);
+      if (mine) store_row(p, acc, stg, plane, row0, n);
     }
     if (lane == 0) bulk_wait_all();
   }
