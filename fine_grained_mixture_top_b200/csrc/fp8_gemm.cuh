@@ -13,7 +13,7 @@
 //
 // Two kernels: tiles of 256 x 256 on pairs of CTAs, and tiles of 128 columns with
 // the operands exchanged where there are few rows.  All waits are bounded
-// (mbar_wait).
+// (mbar_wait, mbar_wait_cl).
 #pragma once
 #include <cuda.h>
 
@@ -555,7 +555,8 @@ __global__ void __maxnreg__((Fp8SmallShape::kMaxReg)) fp8_gemm_small_kernel(cons
 // warpgroup, which gives up most of its registers), 4 .. 11 the epilogue.
 // Barriers: full[s] and slot_empty[b] are the first CTA's (both CTAs' loads and
 // epilogues arrive there); empty[s] and slot_full[b] are each CTA's own, the
-// MMA's commit arriving at both.
+// MMA's commit arriving at both.  All four are signalled across the pair, so
+// every wait acquires at cluster scope.
 struct Fp8PairShape {
   static constexpr int kStage = 2 * kFp8Box;  // per CTA
   static constexpr int kSlots = 2;            // 256-column TMEM slots
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(Fp8PairShape::kThreads, 1) __cluster_dims__(2,
         const int m = t.m0 + 128 * (int)rank, n = t.n0 + 128 * (int)rank;
         for (int kb = 0; kb < t.nkb; ++kb, ++it) {
           const int s = it % S;
-          if (!mbar_wait(smem_u32(&empty[s]), ((it / S) & 1) ^ 1, abort_flag, p.st, 0x389)) {
+          if (!mbar_wait_cl(smem_u32(&empty[s]), ((it / S) & 1) ^ 1, abort_flag, p.st, 0x389)) {
             ok = false;
             break;
           }
@@ -787,12 +788,12 @@ __global__ void __launch_bounds__(Fp8PairShape::kThreads, 1) __cluster_dims__(2,
         const Fp8PairTile t = fp8_pair_tile(p, id, mt, list);
         for (int kb = 0; kb < t.nkb && ok; ++kb, ++it) {
           const int s = it % S;
-          if (!mbar_wait(smem_u32(&full[s]), (it / S) & 1, abort_flag, p.st, 0x38a)) {
+          if (!mbar_wait_cl(smem_u32(&full[s]), (it / S) & 1, abort_flag, p.st, 0x38a)) {
             ok = false;
             break;
           }
           const int b = it % SH::kSlots;
-          if (!mbar_wait(smem_u32(&slot_empty[b]), ((it / SH::kSlots) & 1) ^ 1, abort_flag, p.st, 0x38b)) {
+          if (!mbar_wait_cl(smem_u32(&slot_empty[b]), ((it / SH::kSlots) & 1) ^ 1, abort_flag, p.st, 0x38b)) {
             ok = false;
             break;
           }
@@ -822,7 +823,7 @@ __global__ void __launch_bounds__(Fp8PairShape::kThreads, 1) __cluster_dims__(2,
     bool ok = true;
     auto wait_slot = [&](int i) {
       const int b = i % SH::kSlots;
-      if (!mbar_wait(smem_u32(&slot_full[b]), (i / SH::kSlots) & 1, abort_flag, p.st, 0x38c)) return false;
+      if (!mbar_wait_cl(smem_u32(&slot_full[b]), (i / SH::kSlots) & 1, abort_flag, p.st, 0x38c)) return false;
       tc_fence_after();
       return true;
     };
