@@ -191,6 +191,8 @@ class Routing:
     """Device buffers of a moe_routing, allocated with torch."""
     tensors: dict
     struct: MoeRouting
+    # the pairs are moe_token_round's: in expert order, some of them not in topk_idx
+    rounded: bool = False
 
     def __getitem__(self, k):
         return self.tensors[k]
@@ -222,6 +224,7 @@ def moe_route(dims, opts, X, Wr, bias, routing: Routing, ws, stream=None):
     _check(lib().moe_route(ctypes.byref(dims), ctypes.byref(opts), _ptr(X), _ptr(Wr), _ptr(bias),
                            ctypes.byref(routing.struct), _ptr(ws), ws.numel() * ws.element_size(),
                            _stream(stream)), "moe_route")
+    routing.rounded = False
 
 
 def moe_route_given(dims, opts, routing: Routing, ws, stream=None):
@@ -229,6 +232,7 @@ def moe_route_given(dims, opts, routing: Routing, ws, stream=None):
     routing['topk_gate'] filled by the caller)."""
     _check(lib().moe_route_given(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(routing.struct), _ptr(ws),
                                  ws.numel() * ws.element_size(), _stream(stream)), "moe_route_given")
+    routing.rounded = False
 
 
 def moe_ep_pack(dims, opts, routing: Routing, src, send_rows, send_gate, pair_pos, ws, stream=None):
@@ -254,11 +258,13 @@ def moe_route_noalloc(dims, opts, X, Wr, bias, routing: Routing, stream=None):
     memory; its scratch is a 16 MiB static array in the library (see moe.h)."""
     _check(lib().moe_route_noalloc(ctypes.byref(dims), ctypes.byref(opts), _ptr(X), _ptr(Wr), _ptr(bias),
                                    ctypes.byref(routing.struct), _stream(stream)), "moe_route_noalloc")
+    routing.rounded = False
 
 
 def moe_token_round(dims, opts, routing: Routing, ws, stream=None):
     _check(lib().moe_token_round(ctypes.byref(dims), ctypes.byref(opts), ctypes.byref(routing.struct), _ptr(ws),
                                  ws.numel() * ws.element_size(), _stream(stream)), "moe_token_round")
+    routing.rounded = True
 
 
 def moe_forward(dims, opts, X, W1, W2, routing: Routing, O, H, ws, stream=None):
@@ -518,7 +524,7 @@ def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: b
     ld = _matrix(rows, "rows", R, width, dev)
     ldo = _matrix(dout, "dout", T, width, dev, rows.dtype)
     K = routing.tensors["topk_idx"].shape[1]
-    if not pairs and routing.struct.P_max != T * K:
+    if not pairs and (routing.rounded or routing.struct.P_max != T * K):
         raise ValueError("a routing with token rounding has no place per choice: pass pairs=True")
     if drows is not None and drows.data_ptr() == rows.data_ptr() and drows.numel():
         raise ValueError("drows: must not be rows")
