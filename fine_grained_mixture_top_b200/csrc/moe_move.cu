@@ -55,6 +55,7 @@ struct SortArgs {
   int* pair_expert;
   float* pair_gate;
   int* pair_row;
+  int* pair_slot;  // nullable
   int* counts;
   int* offsets;
   int* row_tok;
@@ -126,6 +127,7 @@ __device__ __forceinline__ void fill_rest(const SortArgs& a, const int* off, con
     a.pair_row[p] = -1;
     a.pair_expert[p] = -1;
     a.pair_gate[p] = 0.f;
+    if (a.pair_slot) a.pair_slot[p] = -1;
   }
   if (blockIdx.x == 0) {
     for (int e = threadIdx.x; e <= a.E; e += kSortThreads) {
@@ -139,11 +141,13 @@ __device__ __forceinline__ void fill_rest(const SortArgs& a, const int* off, con
 // choice i < 2^31 with gate g; `before`: kept choices before it
 __device__ __forceinline__ void scatter_choice(const SortArgs& a, uint32_t i, int e, float g, int row, int64_t before) {
   const int t = (int)(i / (uint32_t)a.K);
-  if (i == (uint32_t)t * (uint32_t)a.K) a.tok_ptr[t] = (int)before;
+  const uint32_t slot = i - (uint32_t)t * (uint32_t)a.K;
+  if (slot == 0) a.tok_ptr[t] = (int)before;
   if (e < 0) return;
   a.pair_row[before] = row;
   a.pair_expert[before] = e;
   a.pair_gate[before] = g;
+  if (a.pair_slot) a.pair_slot[before] = (int)slot;
   a.row_tok[row] = t;
   a.row_gate[row] = g;
 }
@@ -522,12 +526,15 @@ __global__ void __launch_bounds__(256, 4) unpermute_kernel(int T_, int width, co
 // row's products summed in fp32 (per lane, then over the lanes in a fixed
 // order).  A token's pairs are neighbours, so its dout row comes from DRAM
 // once.  The blocks past the pairs zero the padding rows and the gate
-// gradients of dropped choices.
+// gradients of dropped choices.  A pair's slot is the one its sort wrote; in a
+// routing without these, a token with K pairs has them in slot order, and one
+// with fewer has them in the order of topk_idx's choices inside [0, E).
 struct UnpermuteBwdArgs {
   int64_t T, P_max;
   int width, E, K;
   unsigned pair_blocks, pad_blocks;
   const int *tok_ptr, *pair_row, *row_tok, *offsets, *counts, *topk_idx;
+  const int* pair_slot;  // nullable
   const float* pair_gate;
   float *pair_dgate, *topk_dgate;  // each nullable
   int64_t ld_dout, ld_rows, ld_drows;
@@ -539,10 +546,20 @@ __global__ void __launch_bounds__(256, 4) unpermute_bwd_kernel(const UnpermuteBw
   constexpr int V = kVec<T>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x >= a.pair_blocks + a.pad_blocks) {
-    const int64_t n = a.T * a.K;
     const int64_t step = (int64_t)(gridDim.x - a.pair_blocks - a.pad_blocks) * 256;
-    for (int64_t i = (int64_t)(blockIdx.x - a.pair_blocks - a.pad_blocks) * 256 + threadIdx.x; i < n; i += step)
-      if ((unsigned)__ldg(a.topk_idx + i) >= (unsigned)a.E) a.topk_dgate[i] = 0.f;
+    for (int64_t t = (int64_t)(blockIdx.x - a.pair_blocks - a.pad_blocks) * 256 + threadIdx.x; t < a.T; t += step) {
+      const int p0 = __ldg(a.tok_ptr + t), p1 = __ldg(a.tok_ptr + t + 1);
+      if (p1 - p0 == a.K) continue;
+      unsigned kept = 0;
+      if (a.pair_slot) {
+        for (int p = p0; p < p1; ++p) kept |= 1u << (__ldg(a.pair_slot + p) & 31);
+      } else {
+        for (int k = 0; k < a.K; ++k)
+          if ((unsigned)__ldg(a.topk_idx + t * a.K + k) < (unsigned)a.E) kept |= 1u << k;
+      }
+      for (int k = 0; k < a.K; ++k)
+        if (!(kept >> k & 1)) a.topk_dgate[t * a.K + k] = 0.f;
+    }
     return;
   }
   if (blockIdx.x >= a.pair_blocks) {
@@ -606,11 +623,17 @@ __global__ void __launch_bounds__(256, 4) unpermute_bwd_kernel(const UnpermuteBw
   for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
   if (a.pair_dgate && lane == 0) a.pair_dgate[p] = dot;
   if (a.topk_dgate) {
-    // the pair's slot: its place among the token's kept choices
-    const int v = lane < a.K ? __ldg(a.topk_idx + (int64_t)t * a.K + lane) : -1;
-    unsigned kept = __ballot_sync(0xffffffffu, (unsigned)v < (unsigned)a.E);
-    for (int64_t j = p - __ldg(a.tok_ptr + t); j > 0; --j) kept &= kept - 1;
-    if (lane == 0 && kept) a.topk_dgate[(int64_t)t * a.K + __ffs(kept) - 1] = dot;
+    const int p0 = __ldg(a.tok_ptr + t);
+    int slot = (int)p - p0;
+    if (a.pair_slot) {
+      slot = __ldg(a.pair_slot + p);
+    } else if (__ldg(a.tok_ptr + t + 1) - p0 != a.K) {
+      const int v = lane < a.K ? __ldg(a.topk_idx + (int64_t)t * a.K + lane) : -1;
+      unsigned kept = __ballot_sync(0xffffffffu, (unsigned)v < (unsigned)a.E);
+      for (int j = slot; j > 0; --j) kept &= kept - 1;
+      slot = __ffs(kept) - 1;
+    }
+    if (lane == 0 && (unsigned)slot < (unsigned)a.K) a.topk_dgate[(int64_t)t * a.K + slot] = dot;
   }
 }
 
@@ -660,7 +683,7 @@ cudaError_t launch_unpermute_bwd(UnpermuteBwdArgs a, const void* dout, const voi
   const int64_t elems[] = {a.width, a.ld_dout, a.ld_rows, a.ld_drows};
   a.pair_blocks = (unsigned)cdiv(a.P_max, 8);
   a.pad_blocks = (unsigned)(a.E * kPadSplit);
-  const unsigned extra = a.topk_dgate ? (unsigned)std::min<int64_t>(148, cdiv(a.T * a.K, 256)) : 0;
+  const unsigned extra = a.topk_dgate ? (unsigned)std::min<int64_t>(148, cdiv(a.T, 256)) : 0;
   const dim3 grid(a.pair_blocks + a.pad_blocks + extra);
   if (whole_pieces(ptrs, 3, elems, 4, sizeof(T)))
     return launch_pdl(unpermute_bwd_kernel<T, true>, grid, dim3(256), 0, s, a, static_cast<const T*>(dout),
@@ -742,6 +765,7 @@ moe_status moe_sort_pairs(int64_t T, int32_t E, int32_t K, const moe_routing* rt
   const void* req[] = {rt->pair_expert, rt->row_gate, rt->tile_expert};
   for (const void* q : req)
     if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(rt->pair_slot)) return MOE_ERR_INVALID_ARG;
   if (P > 0 && (!rt->topk_idx || !rt->topk_gate || (reinterpret_cast<uintptr_t>(rt->topk_idx) & 3u) ||
                 (reinterpret_cast<uintptr_t>(rt->topk_gate) & 3u)))
     return MOE_ERR_INVALID_ARG;
@@ -763,6 +787,7 @@ moe_status moe_sort_pairs(int64_t T, int32_t E, int32_t K, const moe_routing* rt
   a.pair_expert = rt->pair_expert;
   a.pair_gate = rt->pair_gate;
   a.pair_row = rt->pair_row;
+  a.pair_slot = rt->pair_slot;
   a.counts = rt->counts;
   a.offsets = rt->offsets;
   a.row_tok = rt->row_tok;
@@ -849,7 +874,8 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
   if (!rows_ok(dout, ld_dout, width, type) || !rows_ok(rows, ld_rows, width, type) ||
       !rows_ok(drows, ld_drows, width, type))
     return MOE_ERR_INVALID_ARG;
-  if (topk_dgate && !rt->topk_idx) return MOE_ERR_INVALID_ARG;
+  if (topk_dgate && !rt->topk_idx && !rt->pair_slot) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(rt->pair_slot)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   UnpermuteBwdArgs a;
   a.T = T;
@@ -863,6 +889,7 @@ moe_status moe_unpermute_bwd(int64_t T, int32_t E, int32_t K, const moe_routing*
   a.offsets = rt->offsets;
   a.counts = rt->counts;
   a.topk_idx = rt->topk_idx;
+  a.pair_slot = rt->pair_slot;
   a.pair_gate = rt->pair_gate;
   a.pair_dgate = pair_dgate;
   a.topk_dgate = topk_dgate;

@@ -37,7 +37,8 @@ _ROUTING_PTRS = ["logits", "probs", "topk_idx", "topk_gate", "tok_ptr", "pair_ex
 
 class MoeRouting(ctypes.Structure):
     _fields_ = [(name, c_void_p) for name in _ROUTING_PTRS] + [("P_max", c_int64), ("R_max", c_int64),
-                                                                ("pair_dS", c_void_p)]
+                                                                ("pair_dS", c_void_p),
+                                                                ("pair_slot", c_void_p)]
 
 
 class MoeSizes(ctypes.Structure):
@@ -415,10 +416,11 @@ def _current(device) -> int:
 
 def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=None, stream=None) -> Routing:
     """Sort the choices topk_idx [T, K] (int32; outside [0, E): dropped) with
-    gates topk_gate [T, K] (fp32) by expert: see moe_sort_pairs in moe.h.  A
-    Routing of an earlier call with the same T, K and E can be given again as
-    `routing`; it is overwritten.  ws: a uint8 workspace of moe_sort_sizes'
-    bytes (default: allocated); calls that may overlap need one each."""
+    gates topk_gate [T, K] (fp32) by expert: see moe_sort_pairs in moe.h.  Both
+    are read by this call alone.  A Routing of an earlier call with the same T, K
+    and E can be given again as `routing`; it is overwritten.  ws: a uint8
+    workspace of moe_sort_sizes' bytes (default: allocated); calls that may
+    overlap need one each."""
     torch = _th()
     dev = topk_idx.device
     T, K = _shape2(topk_idx, "topk_idx")
@@ -436,7 +438,8 @@ def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=N
             i32, f32 = torch.int32, torch.float32
             sizes = {"tok_ptr": (T + 1, i32), "pair_expert": (P.value, i32), "pair_gate": (P.value, f32),
                      "pair_row": (P.value, i32), "counts": (E, i32), "offsets": (E + 1, i32),
-                     "row_tok": (R.value, i32), "row_gate": (R.value, f32), "tile_expert": (R.value // 128, i32)}
+                     "row_tok": (R.value, i32), "row_gate": (R.value, f32), "tile_expert": (R.value // 128, i32),
+                     "pair_slot": (P.value, i32)}
             # at least one element each, so that every pointer is one even without tokens
             whole = {k: torch.empty(max(n, 1), dtype=dt, device=dev) for k, (n, dt) in sizes.items()}
             st = MoeRouting(**{k: _ptr(t) for k, t in whole.items()}, P_max=P.value, R_max=R.value)
@@ -514,7 +517,7 @@ def unpermute(routing: Routing, rows, out=None, stream=None):
 
 def unpermute_bwd(routing: Routing, dout, rows, drows=None, dgate=None, pairs: bool = False, stream=None):
     """Gradients of unpermute: (drows [R_max, width], dgate).  dgate is [T, K]
-    in the places of topk_idx, 0 for dropped choices; with pairs=True it is
+    in the places of the choices, 0 for dropped ones; with pairs=True it is
     [P_max] in pair order (for moe_token_round's routings), where entries past
     the pairs in use are left as they were."""
     torch = _th()

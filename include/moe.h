@@ -87,6 +87,10 @@ typedef struct {
  *   pair_dS[P_max] (nullable)          if set, moe_backward writes the router
  *                                      score gradient dS of every pair there
  *                                      (fp32), with or without router_grad
+ *   pair_slot[P_max] (nullable)        if set, moe_sort_pairs writes each pair's
+ *                                      place among its token's K choices there,
+ *                                      and moe_unpermute_bwd reads it; no other
+ *                                      call looks at it
  */
 typedef struct {
   float* logits;
@@ -105,6 +109,7 @@ typedef struct {
   int64_t P_max;
   int64_t R_max;
   float* pair_dS;
+  int32_t* pair_slot;
 } moe_routing;
 
 typedef struct {
@@ -337,10 +342,11 @@ typedef enum {
  * is dropped: it gets no pair and no row, and a token may lose all its
  * choices.  A token may choose an expert twice and then has two rows there.
  * Fills tok_ptr, pair_expert, pair_gate, pair_row (the kept choices in (t, k)
- * order), counts, offsets, row_tok, row_gate, tile_expert as moe_routing
- * describes them (rows of an expert in (t, k) order), and beyond the used rows
- * and pairs, up to R_max and P_max: row_tok, tile_expert, pair_row and
- * pair_expert -1, row_gate and pair_gate 0.  logits and probs are not touched.
+ * order), counts, offsets, row_tok, row_gate, tile_expert and, if set, pair_slot
+ * as moe_routing describes them (rows of an expert in (t, k) order), and beyond
+ * the used rows and pairs, up to R_max and P_max: row_tok, tile_expert,
+ * pair_row, pair_expert and pair_slot -1, row_gate and pair_gate 0.  logits and
+ * probs are not touched.
  * moe_sort_sizes: capacities (P_max = T K, R_max a multiple of 128) and the
  * bytes of ws, which may be 0 (then ws may be NULL).  1 <= K <= 32; T may be 0.
  */
@@ -368,9 +374,11 @@ moe_status moe_permute_bwd(int64_t T, int32_t E, const moe_routing* rt, moe_dtyp
  *   offsets[E] on left as they were;
  *   the gate gradients <dout[t], rows[r]> (fp32) as pair_dgate[P_max] in pair
  *   order (entries past the pairs in use are left) and/or topk_dgate[T,K] in
- *   the places of rt->topk_idx, 0 for dropped choices (each nullable;
- *   topk_dgate is for routings whose pairs are the kept choices in slot order:
- *   any but moe_token_round's).
+ *   the places of the choices, 0 for dropped ones (each nullable; topk_dgate is
+ *   for routings whose pairs are the kept choices in slot order: any but
+ *   moe_token_round's).  Places come from rt->pair_slot; where that is not set
+ *   and a token has fewer than K pairs, from rt->topk_idx, which must then
+ *   still hold the selection that was sorted.
  */
 moe_status moe_unpermute(int64_t T, int32_t E, const moe_routing* rt, moe_dtype type, int64_t width, const void* rows,
                          int64_t ld_rows, void* out, int64_t ld_out, void* stream);
