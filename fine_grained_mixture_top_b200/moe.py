@@ -427,6 +427,8 @@ def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=N
     for t, name, dt in ((topk_idx, "topk_idx", torch.int32), (topk_gate, "topk_gate", torch.float32)):
         if _matrix(t, name, T, K, dev, dt) != K:
             raise ValueError(f"{name}: must be contiguous")
+    if ws is not None and (ws.dtype != torch.uint8 or ws.device != dev or not ws.is_contiguous()):
+        raise ValueError(f"ws: contiguous uint8 on {dev} expected")
     if _elsewhere(dev, stream):
         return _there(dev, stream, sort_pairs, topk_idx, topk_gate, E, routing, ws)
     if routing is None or ws is None:
@@ -445,8 +447,6 @@ def sort_pairs(topk_idx, topk_gate, E: int, routing: Routing | None = None, ws=N
             st = MoeRouting(**{k: _ptr(t) for k, t in whole.items()}, P_max=P.value, R_max=R.value)
             routing = Routing({**{k: t[:sizes[k][0]] for k, t in whole.items()}, "logits": None, "probs": None,
                                "pair_dS": None}, st)
-    elif ws.dtype != torch.uint8 or ws.device != dev:
-        raise ValueError(f"ws: uint8 on {dev} expected")
     r, st = routing.tensors, routing.struct
     if r.get("logits") is not None or r.get("probs") is not None:
         raise ValueError("routing: not one that sort_pairs made")
