@@ -923,7 +923,9 @@ class MoELayer:
         X is quantized into expert order and A = SwiGLU(H) per row, with an fp32
         scale per 128 values.  O and the saved H (bf16) as forward leaves them, so
         that backward follows unchanged."""
-        import torch
+        torch = _th()
+        if _elsewhere(X.device, stream):
+            return _there(X.device, stream, self.forward_fp8, X, wq, None, O)
         rt, (w1, s1, w2, s2) = self.routing, wq
         O = self.O if O is None else O
         d, n, R = self.dims.d, self.dims.n, self.sizes.R_max
@@ -934,11 +936,11 @@ class MoELayer:
                 "a": _new_codes((R,), n, dev), "sa": torch.empty(-(-n // 128), R, dtype=torch.float32, device=dev),
                 "Y": torch.empty(R, d, dtype=torch.bfloat16, device=dev)}
         b, used = self.ws_fp8, rt["offsets"][self.dims.E:]
-        fp8_quantize_rows(X, row_src=rt["row_tok"], rows_used=used, codes=b["x"], scales=b["sx"], stream=stream)
-        fp8_gemm(b["x"], b["sx"], w1, s1, routing=rt, out=self.H, stream=stream)
-        fp8_quantize_rows(self.H, rows_used=used, swiglu=True, codes=b["a"], scales=b["sa"], stream=stream)
-        fp8_gemm(b["a"], b["sa"], w2, s2, routing=rt, out=b["Y"], stream=stream)
-        return unpermute(rt, b["Y"], out=O, stream=stream)
+        fp8_quantize_rows(X, row_src=rt["row_tok"], rows_used=used, codes=b["x"], scales=b["sx"])
+        fp8_gemm(b["x"], b["sx"], w1, s1, routing=rt, out=self.H)
+        fp8_quantize_rows(self.H, rows_used=used, swiglu=True, codes=b["a"], scales=b["sa"])
+        fp8_gemm(b["a"], b["sa"], w2, s2, routing=rt, out=b["Y"])
+        return unpermute(rt, b["Y"], out=O)
 
     def backward(self, dO, X, Wr, W1, W2, stream=None, grad_events=None, dX=None):
         """dX: output buffer [T, d] bf16 (default: self.dX)."""
