@@ -877,6 +877,12 @@ class MoELayer:
         self.dW2 = torch.empty(E, n, d, dtype=bf, device=device)
         self.dWr = torch.empty(d, E, dtype=torch.float32, device=device)
 
+    def _bytes(self, n, stream):
+        """Memory that belongs to the stream that uses it (None: the current one)."""
+        torch = _th()
+        with torch.cuda.stream(stream):
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+
     def route(self, X, Wr, bias=None, stream=None):
         moe_route(self.dims, self.opts, X, Wr, bias, self.routing, self.ws_route, stream)
         if self.opts.round_mode:
@@ -886,10 +892,9 @@ class MoELayer:
         O = self.O if O is None else O
         if self.mxfp8 if mxfp8 is None else mxfp8:
             if self.ws_fwd_mx is None:
-                import torch
                 if self.sizes.fwd_mx_ws == 0:
                     raise MoEError(2, "moe_forward_mxfp8 (needs n % 128 == 0)")
-                self.ws_fwd_mx = torch.empty(self.sizes.fwd_mx_ws, dtype=torch.uint8, device=self.device)
+                self.ws_fwd_mx = self._bytes(self.sizes.fwd_mx_ws, stream)
             moe_forward_mxfp8(self.dims, self.opts, X, W1, W2, self.routing, O, self.H, self.ws_fwd_mx, stream)
         else:
             moe_forward(self.dims, self.opts, X, W1, W2, self.routing, O, self.H, self.ws_fwd, stream)
@@ -897,19 +902,17 @@ class MoELayer:
 
     def quantize_weights_mxfp8(self, W1, W2, stream=None):
         """MXFP8 copy of W1, W2 for forward_mxfp8_q (weights that stay fixed)."""
-        import torch
         if self.sizes.mx_weights_bytes == 0:
             raise MoEError(2, "moe_mx_quantize_weights (needs n % 128 == 0)")
-        wq = torch.empty(self.sizes.mx_weights_bytes, dtype=torch.uint8, device=self.device)
+        wq = self._bytes(self.sizes.mx_weights_bytes, stream)
         moe_mx_quantize_weights(self.dims, self.opts, W1, W2, wq, stream)
         return wq
 
     def forward_mxfp8_q(self, X, wq, stream=None, O=None):
         """The MXFP8 forward on weights quantized once by quantize_weights_mxfp8."""
-        import torch
         O = self.O if O is None else O
         if self.ws_fwd_mx is None:
-            self.ws_fwd_mx = torch.empty(self.sizes.fwd_mx_ws, dtype=torch.uint8, device=self.device)
+            self.ws_fwd_mx = self._bytes(self.sizes.fwd_mx_ws, stream)
         moe_forward_mxfp8_q(self.dims, self.opts, X, wq, self.routing, O, self.H, self.ws_fwd_mx, stream)
         return O
 

@@ -55,3 +55,32 @@ def test_forward_fp8_on_a_given_stream():
     assert torch.equal(other, ref)
     assert moe.moe_get_status()[0] == 0
     del graph
+
+
+@pytest.mark.gpu
+def test_mxfp8_workspaces_on_a_given_stream():
+    from fine_grained_mixture_top_b200 import moe
+    from workloads import MoEConfig, make_inputs
+    cfg = MoEConfig("mx_stream", T=500, d=256, E=8, n=128, K=2, w_std=0.05, seed=76)
+    inp = make_inputs(cfg, "cuda")
+
+    def layer():
+        m = moe.MoELayer(cfg.T, cfg.d, cfg.E, cfg.n, cfg.K, seed=cfg.seed)
+        m.route(inp["X"], inp["Wr"], inp["bias"])
+        return m
+    m = layer()
+    ref = m.forward(inp["X"], inp["W1"], inp["W2"], mxfp8=True).clone()
+    assert streams_of([m.ws_fwd_mx]) == {torch.cuda.current_stream().cuda_stream}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    m = layer()
+    torch.cuda.synchronize()
+    O = m.forward(inp["X"], inp["W1"], inp["W2"], mxfp8=True, stream=side)
+    side.synchronize()
+    assert streams_of([m.ws_fwd_mx]) == {side.cuda_stream} and torch.equal(O, ref)
+    m = layer()
+    torch.cuda.synchronize()
+    wq = m.quantize_weights_mxfp8(inp["W1"], inp["W2"], stream=side)
+    O = m.forward_mxfp8_q(inp["X"], wq, stream=side)
+    side.synchronize()
+    assert streams_of([wq, m.ws_fwd_mx]) == {side.cuda_stream} and torch.equal(O, ref)
