@@ -712,7 +712,8 @@ moe_status moe_fp8_gemm_dw(int64_t M, int64_t N, int64_t K, int32_t E, const moe
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0) {  // no tokens: no operands, a gradient of zeros
     if (!C || !aligned16(C) || ldc < N || ldc % 8) return MOE_ERR_INVALID_ARG;
-    if (E > 1024) return MOE_ERR_UNSUPPORTED;
+    if (M >= (int64_t(1) << 31) - 256 || N >= (int64_t(1) << 31) - 256 || E > 1024 || (!rt && E != 1))
+      return MOE_ERR_UNSUPPORTED;  // as with tokens
     MOE_TRY_CUDA(cudaMemset2DAsync(C, (size_t)ldc * 2, 0, (size_t)N * 2, (size_t)(E * M), s));
     return MOE_OK;
   }
