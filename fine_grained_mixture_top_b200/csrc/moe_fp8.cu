@@ -483,7 +483,8 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   ApiRange api_range("moe_fp8_quantize_rows");
   if (rows < 0 || in_rows < 0 || cols < 1 || swiglu < 0 || swiglu > 1) return MOE_ERR_INVALID_ARG;
   const int kb = (int)cdiv(cols, kBlk);
-  if (cols > (1 << 20) || rows * kb >= (int64_t(1) << 31) - 64) return MOE_ERR_UNSUPPORTED;
+  constexpr int64_t kMostBlocks = (int64_t(1) << 31) - 64;
+  if (cols > (1 << 20) || rows >= kMostBlocks || rows * kb >= kMostBlocks) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   const moe_status st = check_quant(type, in, ld_in, (int64_t)cols * (1 + swiglu), codes, ld_codes, cols, scales);
   if (st != MOE_OK) return st;

@@ -728,7 +728,8 @@ bool rows_ok(const void* p, int64_t ld, int64_t width, moe_dtype type) {
 
 moe_status sort_plan(int64_t T, int32_t E, int32_t K, int64_t* P, int64_t* R, size_t* ws) {
   if (T < 0 || E < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-  if (E > 1024 || K > 32 || T * (int64_t)K >= (int64_t(1) << 31) - 4096 * 1024) return MOE_ERR_UNSUPPORTED;
+  constexpr int64_t kMostPairs = (int64_t(1) << 31) - 4096 * 1024;
+  if (E > 1024 || K > 32 || T >= kMostPairs || T * (int64_t)K >= kMostPairs) return MOE_ERR_UNSUPPORTED;
   *P = T * K;
   *R = cdiv(*P + (int64_t)(kTile - 1) * std::min<int64_t>(E, *P), kTile) * kTile;
   const int64_t chunks = cdiv(*P, kSortThreads * sort_steps(*P));
