@@ -446,11 +446,12 @@ cudaError_t launch_gather(const QuantArgs& a, const QuantArgs& once, cudaStream_
 }
 
 int64_t elem_size(moe_dtype t) { return t == MOE_F32 ? 4 : (t == MOE_BF16 || t == MOE_F16) ? 2 : 0; }
+// in may be null where a gather has no input rows: then every row is zeros.
 moe_status check_quant(moe_dtype type, const void* in, int64_t ld_in, int64_t width, const void* codes,
-                       int64_t ld_codes, int64_t code_cols, const float* scales) {
+                       int64_t ld_codes, int64_t code_cols, const float* scales, bool no_input = false) {
   const int64_t es = elem_size(type);
   if (es == 0) return MOE_ERR_INVALID_ARG;
-  if (!in || !codes || !scales || reinterpret_cast<uintptr_t>(in) % (uintptr_t)es || !aligned16(codes) ||
+  if ((!in && !no_input) || !codes || !scales || reinterpret_cast<uintptr_t>(in) % (uintptr_t)es || !aligned16(codes) ||
       (reinterpret_cast<uintptr_t>(scales) & 3u))
     return MOE_ERR_INVALID_ARG;
   if (ld_in < width || ld_codes < code_cols || ld_codes % 16 != 0) return MOE_ERR_INVALID_ARG;
@@ -486,7 +487,8 @@ moe_status moe_fp8_quantize_rows(moe_dtype type, const void* in, int64_t ld_in, 
   constexpr int64_t kMostBlocks = (int64_t(1) << 31) - 64;
   if (cols > (1 << 20) || rows >= kMostBlocks || rows * kb >= kMostBlocks) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
-  const moe_status st = check_quant(type, in, ld_in, (int64_t)cols * (1 + swiglu), codes, ld_codes, cols, scales);
+  const moe_status st = check_quant(type, in, ld_in, (int64_t)cols * (1 + swiglu), codes, ld_codes, cols, scales,
+                                    row_src && in_rows == 0);
   if (st != MOE_OK) return st;
   if (ld_scales < rows) return MOE_ERR_INVALID_ARG;
   QuantArgs a = {};
@@ -540,7 +542,7 @@ moe_status moe_fp8_quantize_cols(moe_dtype type, const void* in, int64_t ld_in, 
   if (rows < 0 || in_rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
   if (cols > (1 << 20) || cdiv(rows, kBlk) > 65535) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
-  const moe_status st = check_quant(type, in, ld_in, cols, codes, ld_codes, rows, scales);
+  const moe_status st = check_quant(type, in, ld_in, cols, codes, ld_codes, rows, scales, row_src && in_rows == 0);
   if (st != MOE_OK) return st;
   if (ld_scales < cols) return MOE_ERR_INVALID_ARG;
   QuantArgs a = {};
