@@ -540,8 +540,8 @@ __global__ void __maxnreg__((Fp8SmallShape::kMaxReg)) fp8_gemm_small_kernel(cons
 // warpgroups' registers.  TMEM holds two 256-column slots.
 //
 // What paces it, per block and CTA in short runs: 615 ns with everything; about
-// 450 without the epilogue's arithmetic and the MMAs (the operands come from L2 at
-// the 85 GB/s that an SM fills its shared memory with), 470 without the operand
+// 450 without the epilogue's arithmetic and the MMAs (32 KB of operands from L2:
+// an SM fills its shared memory with 73 GB/s), 470 without the operand
 // loads and that arithmetic (the MMAs, 512 clocks at the tensor core's peak), 510
 // without the MMAs.  The three overlap through four operand stages and two slots.
 // In long runs the power cap lowers the clock, and a block takes 735 ns.

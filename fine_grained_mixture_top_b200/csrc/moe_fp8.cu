@@ -173,7 +173,8 @@ __device__ __forceinline__ void load16_values(Raw8<T> (&x)[2], const T* row, int
 // At memory's rate the kernel has some 16 instructions and 1/12 of a shared
 // L1 wavefront per value.  With 8 values per lane and scalar maxima it was bound
 // by issue (182 us), with 32 in runs of 8 by L1 wavefronts (120 us); it now takes
-// 110 us (16384 tokens of 2048 bf16 values gathered 8 times).
+// 96 us (16384 tokens of 2048 bf16 values gathered 8 times), and 59 us for 65536
+// rows of 2048 as they lie (6.9 TB/s of reads and writes).
 template <typename T, int LOAD, bool SWIGLU>
 __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const QuantArgs a, const T* __restrict__ in) {
   pdl_wait();
@@ -385,7 +386,7 @@ cudaError_t launch_tiles(const QuantArgs& a, int E, const void* in, cudaStream_t
 // 16-byte pieces of blockDim.x columns; blocks of the first column part take
 // their rows' scales.  (One row per thread and blocks for the scales: the
 // gather of 16384 tokens of 2048 values to 131072 rows took 137 us in all where
-// this takes 87, and quantizing every copied row 110.)
+// this takes 85, and quantizing every copied row 96.)
 constexpr int kGatherRows = 8;
 __global__ void __launch_bounds__(256) fp8_gather_kernel(const QuantArgs a, const uint8_t* __restrict__ codes,
                                                          int64_t ld, const float* __restrict__ scales,

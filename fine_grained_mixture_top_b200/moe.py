@@ -615,7 +615,10 @@ def _quantize(cols_form, x, row_src, rows_used, swiglu, codes, scales, stream):
         # Rows that repeat often are quantized once and their codes copied (us, row by
         # row / once: 32 x 7168 to 32768 rows 57 / 29, 4096 x 7168 to 65280 128 / 94);
         # not with few repeats (4096 x 7168 to 16384: 34 / 38) or little to copy
-        # (1 x 2048 to 1024: 2.1 / 3.8, to 8192: 5.1 / 5.4).
+        # (1 x 2048 to 1024: 2.1 / 3.8, to 8192: 5.1 / 5.4).  The rows in use are
+        # not known here; where they are few it still pays, since the blocks of
+        # the others are fewer (512 x 2048 to 512 of 33024: 9.5 / 6.7,
+        # 64 x 7168 to 1024 of 33024: 31 / 7.9).
         if src is not None and rows >= 6 * n_in > 0 and rows * cols > 1 << 24:
             need = lib().moe_fp8_gather_ws(n_in, cols)
             ws = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -637,7 +640,7 @@ def fp8_quantize_rows(x, row_src=None, rows_used=None, swiglu: bool = False, cod
 def fp8_quantize_cols(x, row_src=None, rows_used=None, codes=None, scales=None, stream=None):
     """x [rows, cols] -> (codes [cols, rows], scales [ceil(rows / 128), cols]):
     one scale per column and 128 rows, codes transposed.  row_src and rows_used
-    as in fp8_quantize_rows."""
+    as in fp8_quantize_rows.  At most 65535 x 128 rows."""
     return _quantize(True, x, row_src, rows_used, False, codes, scales, stream)
 
 
